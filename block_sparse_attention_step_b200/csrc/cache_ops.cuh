@@ -1,0 +1,39 @@
+// Parameter blocks and launchers of the paged-cache operators: rotary append,
+// decode over an 8-bit cache, sliding-window attention (internal).
+#pragma once
+
+#include "seer_kernels.cuh"
+
+namespace seer {
+
+// Rotary append of a ragged batch's new tokens to the paged cache.
+struct AppendParams {
+  const uint16_t* q;  // optional
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+  const int32_t* cu;         // [B + 1], or nullptr: one token per sequence
+  const int32_t* positions;  // optional [T]
+  const int32_t* seqlens;
+  const int32_t* page_table;
+  const float* rope;  // [max_position][rot], nullptr when rot == 0
+  uint16_t* q_out;
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;  // [num_pages][Hkv], 8-bit cache
+  float* v_scale;
+  float* kbar;  // optional
+  int32_t* status;
+  int B, Hq, Hkv, bs, max_blocks, T, max_new, max_position, rot, interleaved;
+  int64_t num_pages, stride_page, stride_token, stride_head;
+  // set by the launcher
+  int rows_kv;      // the row role writes k and v too (bf16, no pooled keys)
+  int tile_tokens;  // tokens of a row-role tile
+  int items;        // touched blocks at most
+};
+
+cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream);
+cudaError_t run_rope_table(float* table, int max_position, int rot, double base,
+                           cudaStream_t stream);
+
+}  // namespace seer

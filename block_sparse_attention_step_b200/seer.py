@@ -27,6 +27,13 @@ DEV_BAD_INDEX = 2
 DEV_BAD_PAGE = 4
 DEV_K_CLAMPED = 8
 DEV_TIMEOUT = 16
+DEV_NONFINITE_KV = 32
+DEV_BAD_TOKENS = 64
+DEV_BAD_POSITION = 128
+
+CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2
+_CACHE_TYPES = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3,
+                torch.int8: CACHE_INT8}
 
 EXPORTS = (
     "seer_version", "seer_status_string", "seer_last_cuda_error", "seer_dims_default",
@@ -40,6 +47,7 @@ EXPORTS = (
     "seer_prefill_k_max", "seer_prefill_workspace_bytes", "seer_prefill",
     "seer_prefill_attention",
     "seer_block_lse_elems", "seer_sparse_decode_mass", "seer_block_mass",
+    "seer_rope_table", "seer_append_rope",
 )
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -88,6 +96,21 @@ class seer_prefill_args(ctypes.Structure):
                 ("scores_out", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
+class seer_append_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("cu_tokens", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("rope", ctypes.c_void_p), ("total_tokens", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_position", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("cache_type", ctypes.c_int32), ("k_pool", ctypes.c_void_p),
+                ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("kbar", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(seer_dims)
 _I = ctypes.c_int32
@@ -122,6 +145,8 @@ _SIGS = {
     "seer_sparse_decode_mass": (_I, [_D, _P, _P, _P, _P, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P,
                                      _P, _P, _P, _P]),
     "seer_block_mass": (_I, [_D, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "seer_rope_table": (_I, [_I, _I, ctypes.c_double, _P, _P]),
+    "seer_append_rope": (_I, [_D, ctypes.POINTER(seer_append_args), _P]),
 }
 
 _lib_handle = None
@@ -420,3 +445,117 @@ def seer_prefill(d, q, k_pool, v_pool, page_table, seqlens, w_gate, kbar, *, poo
     a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
     _check("seer_prefill", _lib().seer_prefill(ctypes.byref(d), ctypes.byref(a), _stream(stream)))
 
+
+
+# ------------------------------------------------------------ paged KV cache
+def _keep(a, *tensors):
+    """Argument blocks of the cache operators hold on to their tensors and
+    remember the device these are on."""
+    live = [t for t in tensors if t is not None]
+    devices = {t.device for t in live}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on more than one device: {sorted(map(str, devices))}")
+    a.tensors = live
+    a.device = devices.pop().index
+    return a
+
+
+def _call(fn: str, d, a, stream):
+    """A cache operator on its tensors' device, which has to be the current one."""
+    if a.device != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors on cuda:{a.device}, current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    status = getattr(_lib(), fn)(ctypes.byref(d), ctypes.byref(a), _stream(stream))
+    if status != SEER_OK:
+        raise SeerError(fn, status)
+
+
+def _cache(a, k_pool, v_pool, k_scale, v_scale):
+    if k_pool.dtype not in _CACHE_TYPES:
+        raise TypeError(f"k_pool must be bfloat16, float8_e4m3fn or int8, got {k_pool.dtype}")
+    a.cache_type = _CACHE_TYPES[k_pool.dtype]
+    a.k_pool = _ptr(k_pool, k_pool.dtype, "k_pool")
+    a.v_pool = _ptr(v_pool, k_pool.dtype, "v_pool")
+    eight = a.cache_type != CACHE_BF16
+    if not eight and (k_scale is not None or v_scale is not None):
+        raise ValueError("a bfloat16 cache has no scales")
+    a.k_scale = _ptr(k_scale, torch.float32, "k_scale", allow_none=not eight)
+    a.v_scale = _ptr(v_scale, torch.float32, "v_scale", allow_none=not eight)
+
+
+def _rows(t, name):
+    """(pointer, elements between tokens) of [T][H][D] bf16 rows whose heads
+    are D apart; the tokens may be further apart (a fused projection)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][head_dim]")
+    T, H, D = t.shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)
+                      or (T > 1 and t.stride(0) < H * D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else H * D)
+
+
+def seer_rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, table=None,
+                    device=None, stream=None):
+    """[max_position][rotary_dim] fp32 table of a position rotation (cosines,
+    then sines), allocated unless given."""
+    if table is None:
+        table = torch.empty((max_position, rotary_dim), dtype=torch.float32,
+                            device=device or torch.device("cuda", torch.cuda.current_device()))
+    if tuple(table.shape) != (max_position, rotary_dim):
+        raise ValueError("table must be [max_position][rotary_dim]")
+    _check("seer_rope_table", _lib().seer_rope_table(
+        int(max_position), int(rotary_dim), float(base), _ptr(table, torch.float32, "table"),
+        _stream(stream)))
+    return table
+
+
+def append_args(k_new, v_new, k_pool, v_pool, page_table, seqlens, *, q=None, q_out=None,
+                rope=None, interleaved=False, cu_tokens=None, max_new=1, positions=None,
+                k_scale=None, v_scale=None, kbar=None, dev_status=None) -> seer_append_args:
+    """Arguments of seer_append_rope: [T][heads][D] bf16 rows of q (optional),
+    k and v, a cache in bfloat16, float8_e4m3fn or int8 (with its scales), and
+    the rotation table (None: no rotation)."""
+    a = seer_append_args()
+    a.k_new, a.k_stride = _rows(k_new, "k_new")
+    a.v_new, a.v_stride = _rows(v_new, "v_new")
+    if k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new differ in shape")
+    if q is not None:
+        a.q, a.q_stride = _rows(q, "q")
+        if q.shape[0] != k_new.shape[0]:
+            raise ValueError("q and k_new differ in tokens")
+        if q_out is None:
+            raise ValueError("q_out is required with q")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        if q_out.data_ptr() == q.data_ptr():
+            a.q_out, out_stride = _rows(q_out, "q_out")
+            if out_stride != a.q_stride:
+                raise ValueError("q_out over q must have q's strides")
+        else:
+            a.q_out = _ptr(q_out, torch.bfloat16, "q_out")
+    _cache(a, k_pool, v_pool, k_scale, v_scale)
+    a.cu_tokens = _ptr(cu_tokens, torch.int32, "cu_tokens", allow_none=True)
+    a.positions = _ptr(positions, torch.int32, "positions", allow_none=True)
+    a.rope = _ptr(rope, torch.float32, "rope", allow_none=True)
+    a.total_tokens = k_new.shape[0]
+    a.max_new = int(max_new)
+    if rope is not None:
+        a.max_position, a.rotary_dim = rope.shape
+    a.interleaved = int(bool(interleaved))
+    a.page_table = _ptr(page_table, torch.int32, "page_table", allow_none=True)
+    a.seqlens = _ptr(seqlens, torch.int32, "seqlens")
+    a.kbar = _ptr(kbar, torch.float32, "kbar", allow_none=True)
+    a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
+    return _keep(a, k_new, v_new, k_pool, v_pool, page_table, seqlens, q, q_out, rope, cu_tokens,
+                 positions, k_scale, v_scale, kbar, dev_status)
+
+
+def seer_append_rope(d, args: seer_append_args, stream=None):
+    """Rotate new q / k rows and append k / v to the paged cache."""
+    _call("seer_append_rope", d, args, stream)

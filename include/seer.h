@@ -97,6 +97,11 @@ typedef enum seer_status {
 #define SEER_DEV_BAD_PAGE 4        /* page outside [0, num_pages): page 0 used */
 #define SEER_DEV_K_CLAMPED 8       /* k_per_seq[b] > k_max: clamped to k_max */
 #define SEER_DEV_TIMEOUT 16        /* a pipeline wait gave up after ~1 s */
+#define SEER_DEV_NONFINITE_KV 32   /* a new key or value was NaN or +-inf */
+#define SEER_DEV_BAD_TOKENS 64     /* token offsets and lengths that do not fit:
+                                      the sequence is left out */
+#define SEER_DEV_BAD_POSITION 128  /* a position outside the rotation table:
+                                      its nearest row is used */
 
 typedef struct seer_dims {
   int32_t batch;        /* B >= 1 */
@@ -472,6 +477,84 @@ SEER_API seer_status seer_step_workspace_init(const seer_dims *d, int32_t k_max,
                                               int32_t num_splits, void *workspace,
                                               size_t workspace_bytes,
                                               seer_stream stream);
+
+/* -------------------------------------------------------- paged KV cache
+ * The types a cache holds its keys and values in.  An 8-bit pool has the
+ * layouts of a bf16 pool with one byte per element (strides in elements, all
+ * multiples of 16) and two fp32 arrays k_scale, v_scale [num_pages][Hkv]: an
+ * element is code * scale of its page and KV head.  Scales are finite and
+ * >= 0; 0 says that the page's rows of that head are all zero. */
+#define SEER_CACHE_BF16 0
+#define SEER_CACHE_E4M3 1 /* 8-bit float, 4 exponent and 3 mantissa bits, +-448 */
+#define SEER_CACHE_INT8 2 /* two's complement, -127 .. 127 */
+
+/* Table of a position rotation: row pos of table [max_position][rotary_dim]
+ * holds cos, then sin, of pos * base^(-2 i / rotary_dim), i = 0 ..
+ * rotary_dim / 2 - 1 (angles in fp64).  A caller with another rule for its
+ * angles fills the table itself. */
+SEER_API seer_status seer_rope_table(int32_t max_position, int32_t rotary_dim,
+                                     double base, float *table, seer_stream stream);
+
+/* Append of new tokens to the paged cache with the position rotation applied
+ * on the way, for a decode batch, a prompt or ragged chunks of prompts.
+ *
+ * Rows cu_tokens[b] .. cu_tokens[b+1] - 1 of q, k_new and v_new are the n_b
+ * new tokens of sequence b (0 <= n_b <= max_new); cu_tokens NULL: row b is the
+ * one new token of sequence b, or nothing where seqlens[b] is 0.  seqlens
+ * already counts them, so token i lies at cache position seqlens[b] - n_b + i.
+ * Rows behind the last sequence and those of a sequence whose offsets or
+ * length do not fit (flagged SEER_DEV_BAD_TOKENS) are left out: nothing is
+ * written for them.  A row whose page is outside the pool is left out too
+ * (SEER_DEV_BAD_PAGE).
+ *
+ * The first rotary_dim dims of each q and k row are turned in pairs (x, y) ->
+ * (x c - y s, y c + x s) by the table row of the token's position: dims i and
+ * i + rotary_dim / 2, or 2 i and 2 i + 1 when interleaved.  rope NULL with
+ * rotary_dim 0: no rotation.  Arithmetic in fp32, rounded once at the end.
+ *
+ * 8-bit cache: with amax the largest finite magnitude of a block's new rows
+ * of one head, a block without earlier rows gets the scale 2^k, the least
+ * with amax <= 448 * 2^k (e4m3), or amax / 127 (int8); a block with earlier
+ * rows keeps its scale, doubled until amax fits, and its earlier codes are
+ * rounded again where it grew.  Codes are round-to-nearest-even of value /
+ * scale.  NaN and +-inf are flagged (SEER_DEV_NONFINITE_KV) and stored as NaN
+ * (int8: 0) and the largest code.
+ *
+ * kbar, if not NULL, receives the pooled keys of every block that got rows:
+ * the mean of the block's rows as the cache now holds them (for a bf16 cache
+ * the bits of seer_pool_keys).
+ *
+ * A page that receives rows belongs to one sequence.  Calls that write the
+ * same pages are ordered by the caller.  q_out may be q. */
+typedef struct seer_append_args {
+  const uint16_t *q;         /* [T][Hq][D] bf16, or NULL with q_out */
+  const uint16_t *k_new;     /* [T][Hkv][D] bf16 */
+  const uint16_t *v_new;
+  int64_t q_stride;          /* elements between two tokens' rows, multiples of 8; */
+  int64_t k_stride;          /* 0: contiguous (so rows of one fused projection need */
+  int64_t v_stride;          /* no copy).  Heads of a token are D elements apart. */
+  uint16_t *q_out;           /* [T][Hq][D], contiguous unless it is q */
+  const int32_t *cu_tokens;  /* [B + 1], or NULL (then total_tokens = B, max_new = 1) */
+  const int32_t *positions;  /* [T] table rows, or NULL: the cache positions */
+  const float *rope;         /* [max_position][rotary_dim], 16-byte aligned */
+  int32_t total_tokens;      /* T: rows of q, k_new, v_new */
+  int32_t max_new;           /* >= every n_b */
+  int32_t max_position;
+  int32_t rotary_dim;        /* a multiple of 16, <= D */
+  int32_t interleaved;
+  int32_t cache_type;        /* SEER_CACHE_* */
+  void *k_pool;
+  void *v_pool;
+  float *k_scale;            /* 8-bit cache only */
+  float *v_scale;
+  const int32_t *page_table; /* may be NULL (identity) */
+  const int32_t *seqlens;
+  float *kbar;               /* may be NULL */
+  int32_t *dev_status;       /* may be NULL */
+} seer_append_args;
+
+SEER_API seer_status seer_append_rope(const seer_dims *d, const seer_append_args *a,
+                                      seer_stream stream);
 
 #ifdef __cplusplus
 }
