@@ -26,9 +26,153 @@ seer_status check_cache(const seer_dims* d, int cache, const void* k_pool, const
   return SEER_OK;
 }
 
+// Pool tensor map of an 8-bit cache: dims (D, head, token, page) or (D, token,
+// head, page), whichever lists the smaller stride first; box = one head's 64
+// tokens of 128 bytes, 128-byte swizzle.
+seer_status make_code_map(const void* base, const seer_dims* d, int token_inner,
+                          CUtensorMap* map) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return SEER_ERR_CUDA;
+  const cuuint64_t heads = (cuuint64_t)d->num_kv_heads, tokens = (cuuint64_t)d->block_size;
+  const cuuint64_t sh = (cuuint64_t)d->stride_head, st = (cuuint64_t)d->stride_token;
+  const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, token_inner ? tokens : heads,
+                              token_inner ? heads : tokens, (cuuint64_t)d->num_pages};
+  const cuuint64_t strides[3] = {token_inner ? st : sh, token_inner ? sh : st,
+                                 (cuuint64_t)d->stride_page};
+  const cuuint32_t box[4] = {(cuuint32_t)kHeadDim, token_inner ? (cuuint32_t)kTileTokens : 1u,
+                             token_inner ? 1u : (cuuint32_t)kTileTokens, 1u};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                         strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SEER_OK : SEER_ERR_UNSUPPORTED;
+}
+
+constexpr int kClusterMax = 8;  // CTAs that join one row's pieces without a partial
+
+// Pieces per row: enough CTAs for every SM's resident slots, no piece below
+// two stages.
+int32_t pick_splits(const seer_dims* d, int64_t stages, int ctas_per_sm) {
+  const int64_t rows = (int64_t)d->batch * d->num_kv_heads;
+  const int64_t slots = (int64_t)num_sms_current() * ctas_per_sm;
+  int32_t s = 1;
+  while (s < kMaxSplits && rows * s * 2 <= slots && stages >= 4 * s) s *= 2;
+  return s;
+}
+
+size_t split_bytes(const seer_dims* d, int32_t splits) {
+  if (splits <= kClusterMax) return 0;
+  const size_t parts = (size_t)d->batch * d->num_q_heads * (splits / kClusterMax);
+  return round256(parts * kHeadDim * sizeof(float)) + round256(parts * sizeof(float));
+}
+
+// Checks, tensor maps and parameters of both decode forms, then the launch.
+seer_status cache_decode(const seer_dims* d, const seer_cache_attn_args* a, bool window,
+                         seer_stream stream) {
+  SEER_TRY(check_dims(d));
+  if (a == nullptr || !a->q || !a->seqlens || !a->out) return SEER_ERR_INVALID_ARG;
+  SEER_TRY(check_cache(d, a->cache_type, a->k_pool, a->v_pool, a->k_scale, a->v_scale));
+  if (window) {
+    if (a->window < 1 || a->sinks < 0) return SEER_ERR_INVALID_ARG;
+  } else {
+    if (a->cache_type == SEER_CACHE_BF16) return SEER_ERR_UNSUPPORTED;  // seer_sparse_decode
+    if (!a->idx || !a->n_sel || a->k_max < 1 || a->k_max > d->max_blocks)
+      return SEER_ERR_INVALID_ARG;
+  }
+  const int32_t S = a->num_splits;
+  if (S < 1 || S > kMaxSplits || (S & (S - 1))) return SEER_ERR_INVALID_ARG;
+  if (!aligned(a->q, 16) || !aligned(a->out, 2)) return SEER_ERR_UNSUPPORTED;
+  if ((int64_t)d->batch * d->num_kv_heads * S > INT_MAX) return SEER_ERR_UNSUPPORTED;
+  const size_t need = split_bytes(d, S);
+  if (need > 0 && (a->workspace == nullptr || !aligned(a->workspace, 256) ||
+                   a->workspace_bytes < need))
+    return SEER_ERR_WORKSPACE;
+  CacheDecodeParams p = {};
+  p.token_inner = d->stride_token < d->stride_head ? 1 : 0;
+  CUtensorMap tk, tv;
+  if (a->cache_type == SEER_CACHE_BF16) {
+    SEER_TRY(make_kv_map(static_cast<const uint16_t*>(a->k_pool), d, p.token_inner, &tk));
+    SEER_TRY(make_kv_map(static_cast<const uint16_t*>(a->v_pool), d, p.token_inner, &tv));
+  } else {
+    SEER_TRY(make_code_map(a->k_pool, d, p.token_inner, &tk));
+    SEER_TRY(make_code_map(a->v_pool, d, p.token_inner, &tv));
+  }
+  p.q = a->q;
+  p.page_table = a->page_table;
+  p.seqlens = a->seqlens;
+  p.idx = a->idx;
+  p.n_sel = a->n_sel;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  p.out = a->out;
+  p.lse_out = a->lse_out;
+  p.status = a->dev_status;
+  p.B = d->batch;
+  p.Hq = d->num_q_heads;
+  p.Hkv = d->num_kv_heads;
+  p.G = d->num_q_heads / d->num_kv_heads;
+  p.bs = d->block_size;
+  p.max_blocks = d->max_blocks;
+  p.k_max = a->k_max;
+  p.window = a->window;
+  p.sinks = a->sinks;
+  p.S = S;
+  p.C = S < kClusterMax ? S : kClusterMax;
+  p.num_pages = d->num_pages;
+  p.scale_log2 = a->softmax_scale * kLog2e;
+  if (S > p.C) {
+    const size_t parts = (size_t)d->batch * d->num_q_heads * (S / p.C);
+    p.o_part = static_cast<float*>(a->workspace);
+    p.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) +
+                                          round256(parts * kHeadDim * sizeof(float)));
+  }
+  SEER_CUDA(run_cache_decode(tk, tv, p, a->cache_type, window, stream));
+  if (S > p.C) {
+    CombineParams c = {};
+    c.o_part = p.o_part;
+    c.lse_part = p.lse_part;
+    c.out = a->out;
+    c.lse_out = a->lse_out;
+    c.S = S / p.C;
+    SEER_CUDA(run_combine(c, d->batch, d->num_q_heads, stream, true));
+  }
+  return SEER_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int32_t seer_sparse_decode_q8_splits(const seer_dims* d, int32_t k_max) {
+  if (check_dims(d) != SEER_OK || k_max < 1) return 1;
+  return pick_splits(d, (int64_t)k_max * (d->block_size / kTileTokens), 3);
+}
+
+int32_t seer_window_decode_splits(const seer_dims* d, int32_t window, int32_t sinks) {
+  if (check_dims(d) != SEER_OK || window < 1 || sinks < 0) return 1;
+  int64_t blocks = ((int64_t)sinks + d->block_size - 1) / d->block_size +
+                   ((int64_t)window + d->block_size - 2) / d->block_size + 1;
+  if (blocks > d->max_blocks) blocks = d->max_blocks;
+  return pick_splits(d, blocks * (d->block_size / kTileTokens), 2);
+}
+
+size_t seer_split_workspace_bytes(const seer_dims* d, int32_t num_splits) {
+  if (check_dims(d) != SEER_OK || num_splits < 1 || num_splits > kMaxSplits) return 0;
+  return split_bytes(d, num_splits);
+}
+
+seer_status seer_sparse_decode_q8(const seer_dims* d, const seer_cache_attn_args* a,
+                                  seer_stream stream) {
+  NvtxRange range("seer_sparse_decode_q8");
+  return cache_decode(d, a, false, stream);
+}
+
+seer_status seer_window_decode(const seer_dims* d, const seer_cache_attn_args* a,
+                               seer_stream stream) {
+  NvtxRange range("seer_window_decode");
+  return cache_decode(d, a, true, stream);
+}
 
 seer_status seer_rope_table(int32_t max_position, int32_t rotary_dim, double base, float* table,
                             seer_stream stream) {

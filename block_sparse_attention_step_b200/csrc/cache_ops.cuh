@@ -36,4 +36,29 @@ cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream);
 cudaError_t run_rope_table(float* table, int max_position, int rot, double base,
                            cudaStream_t stream);
 
+// Decode attention over a block list or a window with sinks.
+struct CacheDecodeParams {
+  const uint16_t* q;  // [B][Hq][D]
+  const int32_t* page_table;
+  const int32_t* seqlens;
+  const int32_t* idx;    // [B][Hkv][k_max], list form
+  const int32_t* n_sel;  // [B][Hkv]
+  const float* k_scale;  // [num_pages][Hkv], 8-bit cache
+  const float* v_scale;
+  float* o_part;  // [B][Hq][S / C][D] when S > C, else nullptr
+  float* lse_part;
+  uint16_t* out;
+  float* lse_out;  // optional
+  int32_t* status;
+  int B, Hq, Hkv, G, bs, max_blocks, k_max, window, sinks;
+  int S, C;         // pieces per row, CTAs per cluster (both powers of two, C <= 8 divides S)
+  int token_inner;  // tensor map dims are (D, token, head, page), not (D, head, token, page)
+  int64_t num_pages;
+  float scale_log2;
+};
+
+cudaError_t run_cache_decode(const CUtensorMap& tk, const CUtensorMap& tv,
+                             const CacheDecodeParams& p, int cache, bool window,
+                             cudaStream_t stream);
+
 }  // namespace seer

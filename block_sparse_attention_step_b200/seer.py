@@ -48,6 +48,8 @@ EXPORTS = (
     "seer_prefill_attention",
     "seer_block_lse_elems", "seer_sparse_decode_mass", "seer_block_mass",
     "seer_rope_table", "seer_append_rope",
+    "seer_sparse_decode_q8_splits", "seer_window_decode_splits", "seer_split_workspace_bytes",
+    "seer_sparse_decode_q8", "seer_window_decode",
 )
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -111,6 +113,19 @@ class seer_append_args(ctypes.Structure):
                 ("dev_status", ctypes.c_void_p)]
 
 
+class seer_cache_attn_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("cache_type", ctypes.c_int32),
+                ("num_splits", ctypes.c_int32), ("k_pool", ctypes.c_void_p),
+                ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("idx", ctypes.c_void_p),
+                ("n_sel", ctypes.c_void_p), ("k_max", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("out", ctypes.c_void_p),
+                ("lse_out", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(seer_dims)
 _I = ctypes.c_int32
@@ -147,6 +162,11 @@ _SIGS = {
     "seer_block_mass": (_I, [_D, _P, _P, _I, _P, _P, _P, _P, _P]),
     "seer_rope_table": (_I, [_I, _I, ctypes.c_double, _P, _P]),
     "seer_append_rope": (_I, [_D, ctypes.POINTER(seer_append_args), _P]),
+    "seer_sparse_decode_q8_splits": (_I, [_D, _I]),
+    "seer_window_decode_splits": (_I, [_D, _I, _I]),
+    "seer_split_workspace_bytes": (ctypes.c_size_t, [_D, _I]),
+    "seer_sparse_decode_q8": (_I, [_D, ctypes.POINTER(seer_cache_attn_args), _P]),
+    "seer_window_decode": (_I, [_D, ctypes.POINTER(seer_cache_attn_args), _P]),
 }
 
 _lib_handle = None
@@ -559,3 +579,67 @@ def append_args(k_new, v_new, k_pool, v_pool, page_table, seqlens, *, q=None, q_
 def seer_append_rope(d, args: seer_append_args, stream=None):
     """Rotate new q / k rows and append k / v to the paged cache."""
     _call("seer_append_rope", d, args, stream)
+
+
+def seer_sparse_decode_q8_splits(d, k_max: int) -> int:
+    return _lib().seer_sparse_decode_q8_splits(ctypes.byref(d), int(k_max))
+
+
+def seer_window_decode_splits(d, window: int, sinks: int) -> int:
+    return _lib().seer_window_decode_splits(ctypes.byref(d), int(window), int(sinks))
+
+
+def seer_split_workspace_bytes(d, num_splits: int) -> int:
+    return _lib().seer_split_workspace_bytes(ctypes.byref(d), int(num_splits))
+
+
+def _cache_attn(q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, num_splits, workspace,
+                softmax_scale, out, lse_out, dev_status, *more):
+    a = seer_cache_attn_args()
+    a.q = _ptr(q, torch.bfloat16, "q")
+    _cache(a, k_pool, v_pool, k_scale, v_scale)
+    a.num_splits = int(num_splits)
+    a.page_table = _ptr(page_table, torch.int32, "page_table", allow_none=True)
+    a.seqlens = _ptr(seqlens, torch.int32, "seqlens")
+    a.softmax_scale = float(softmax_scale)
+    if workspace is not None:
+        a.workspace = _ptr(workspace, torch.uint8, "workspace")
+        a.workspace_bytes = workspace.numel()
+    a.out = _ptr(out, torch.bfloat16, "out")
+    a.lse_out = _ptr(lse_out, torch.float32, "lse_out", allow_none=True)
+    a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
+    return _keep(a, q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, workspace, out,
+                 lse_out, dev_status, *more)
+
+
+def sparse_decode_q8_args(q, k_pool, v_pool, page_table, seqlens, idx, n_sel, *, k_scale, v_scale,
+                          k_max, num_splits, softmax_scale, out, workspace=None, lse_out=None,
+                          dev_status=None) -> seer_cache_attn_args:
+    """Arguments of seer_sparse_decode_q8 (float8_e4m3fn or int8 pools)."""
+    a = _cache_attn(q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, num_splits,
+                    workspace, softmax_scale, out, lse_out, dev_status, idx, n_sel)
+    a.idx = _ptr(idx, torch.int32, "idx")
+    a.n_sel = _ptr(n_sel, torch.int32, "n_sel")
+    a.k_max = int(k_max)
+    return a
+
+
+def window_decode_args(q, k_pool, v_pool, page_table, seqlens, *, window, sinks, num_splits,
+                       softmax_scale, out, k_scale=None, v_scale=None, workspace=None,
+                       lse_out=None, dev_status=None) -> seer_cache_attn_args:
+    """Arguments of seer_window_decode (bfloat16, float8_e4m3fn or int8 pools)."""
+    a = _cache_attn(q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, num_splits,
+                    workspace, softmax_scale, out, lse_out, dev_status)
+    a.window = int(window)
+    a.sinks = int(sinks)
+    return a
+
+
+def seer_sparse_decode_q8(d, args: seer_cache_attn_args, stream=None):
+    """Block-sparse decode attention over an 8-bit cache, out and lse in one call."""
+    _call("seer_sparse_decode_q8", d, args, stream)
+
+
+def seer_window_decode(d, args: seer_cache_attn_args, stream=None):
+    """Sliding-window decode attention with sink tokens, out and lse in one call."""
+    _call("seer_window_decode", d, args, stream)

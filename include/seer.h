@@ -556,6 +556,58 @@ typedef struct seer_append_args {
 SEER_API seer_status seer_append_rope(const seer_dims *d, const seer_append_args *a,
                                       seer_stream stream);
 
+/* Decode attention (one query token per sequence) that writes out and lse by
+ * itself.  Tokens t >= seqlens[b] never enter the math and tokens that a row
+ * does not see weigh nothing, whatever the cache holds there.  A row that
+ * sees no token (seqlens[b] or n_sel 0) gets out 0 and lse -inf.
+ *
+ * num_splits (a power of two up to 64) pieces of a row run side by side.  Up
+ * to 8 are joined inside one thread-block cluster; more need a workspace of
+ * seer_split_workspace_bytes() bytes (256-byte aligned, no initial contents;
+ * calls that share one must not overlap).  The *_splits helpers pick a number
+ * for the current device. */
+typedef struct seer_cache_attn_args {
+  const uint16_t *q;         /* [B][Hq][D] bf16, 16-byte aligned */
+  int32_t cache_type;        /* SEER_CACHE_* */
+  int32_t num_splits;
+  const void *k_pool;
+  const void *v_pool;
+  const float *k_scale;      /* [num_pages][Hkv], 8-bit cache only */
+  const float *v_scale;
+  const int32_t *page_table; /* may be NULL (identity) */
+  const int32_t *seqlens;
+  const int32_t *idx;        /* seer_sparse_decode_q8: [B][Hkv][k_max] */
+  const int32_t *n_sel;      /* [B][Hkv] */
+  int32_t k_max;
+  int32_t window;            /* seer_window_decode: >= 1 */
+  int32_t sinks;             /* >= 0 */
+  float softmax_scale;
+  void *workspace;
+  size_t workspace_bytes;
+  uint16_t *out;             /* [B][Hq][D] bf16 */
+  float *lse_out;            /* [B][Hq], may be NULL */
+  int32_t *dev_status;       /* may be NULL */
+} seer_cache_attn_args;
+
+SEER_API int32_t seer_sparse_decode_q8_splits(const seer_dims *d, int32_t k_max);
+SEER_API int32_t seer_window_decode_splits(const seer_dims *d, int32_t window, int32_t sinks);
+SEER_API size_t seer_split_workspace_bytes(const seer_dims *d, int32_t num_splits);
+
+/* seer_sparse_decode and seer_combine in one call, over an 8-bit cache: the
+ * group's query heads attend the tokens of the blocks idx[b,h,0 .. n_sel)
+ * (distinct, as the block selects leave them; entries outside [0, NB_b) are
+ * skipped and flagged, SEER_DEV_BAD_INDEX).  A bf16 cache is
+ * SEER_ERR_UNSUPPORTED (seer_sparse_decode reads it). */
+SEER_API seer_status seer_sparse_decode_q8(const seer_dims *d, const seer_cache_attn_args *a,
+                                           seer_stream stream);
+
+/* Sliding-window decode with sinks, over a cache of any type: the query (at
+ * position seqlens[b] - 1) sees its own and the window - 1 tokens before it,
+ * and the first `sinks` tokens.  A window past the sequence is full
+ * attention.  Only blocks with a visible token are read. */
+SEER_API seer_status seer_window_decode(const seer_dims *d, const seer_cache_attn_args *a,
+                                        seer_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
