@@ -36,6 +36,7 @@
 
 #include "block_mean.cuh"
 #include "cache_ops.cuh"
+#include "ragged.cuh"
 
 namespace seer {
 
@@ -118,32 +119,8 @@ __device__ __forceinline__ float grown_scale(float old, float amax, bool has_old
 }
 
 // ------------------------------------------------------------------- rows
-struct Seq {
-  int first, n, L;  // rows first .. first + n - 1 are its new tokens
-};
-
-// n = 0: nothing to append (an inactive slot, or lengths that do not fit,
-// which are flagged).
 __device__ __forceinline__ Seq load_seq(const AppendParams& p, int b) {
-  Seq s;
-  s.L = __ldg(p.seqlens + b);
-  if (p.cu != nullptr) {
-    s.first = __ldg(p.cu + b);
-    const int end = __ldg(p.cu + b + 1);
-    s.n = end - s.first;
-    if (s.first < 0 || end < s.first || end > p.T || s.n > p.max_new) {
-      flag_status(p.status, SEER_DEV_BAD_TOKENS);
-      s.n = 0;
-    }
-  } else {
-    s.first = b;
-    s.n = s.L == 0 ? 0 : 1;
-  }
-  if (s.n > 0 && (s.L < s.n || s.L > p.max_blocks * p.bs)) {
-    flag_status(p.status, SEER_DEV_BAD_TOKENS);
-    s.n = 0;
-  }
-  return s;
+  return load_seq(p.cu, p.seqlens, b, p.T, p.max_new, p.max_blocks * p.bs, p.status);
 }
 
 // The two chunks of 8 dims a thread (slot 0..7 of its row) holds, and whether

@@ -1,6 +1,8 @@
 // C ABI of the paged-cache operators (rotary append, decode over an 8-bit
 // cache, sliding-window attention): argument checks and launches.  Declared
 // in include/seer.h.
+#include <cmath>
+
 #include "api_util.cuh"
 #include "cache_ops.cuh"
 
@@ -45,6 +47,27 @@ seer_status make_code_map(const void* base, const seer_dims* d, int token_inner,
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
                          strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SEER_OK : SEER_ERR_UNSUPPORTED;
+}
+
+constexpr int kWPTileRows = 128;  // (token, head) rows of a prefill MMA tile
+
+// Packed query rows [T][Hq][D]: dims (D, head, token); box = 64 dims x the
+// group's heads x ntok tokens, 128-byte swizzle.
+seer_status make_rows_map(const uint16_t* q, const seer_dims* d, int T, int ntok,
+                          CUtensorMap* map) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return SEER_ERR_CUDA;
+  const cuuint64_t row = (cuuint64_t)kHeadDim * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)d->num_q_heads, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {row, row * d->num_q_heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(d->num_q_heads / d->num_kv_heads),
+                             (cuuint32_t)ntok};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(q), dims,
+                         strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SEER_OK : SEER_ERR_UNSUPPORTED;
 }
@@ -244,6 +267,49 @@ seer_status seer_append_rope(const seer_dims* d, const seer_append_args* a, seer
   p.stride_token = d->stride_token;
   p.stride_head = d->stride_head;
   SEER_CUDA(run_append_rope(p, a->cache_type, stream));
+  return SEER_OK;
+}
+
+seer_status seer_window_prefill(const seer_dims* d, const seer_window_prefill_args* a,
+                                seer_stream stream) {
+  NvtxRange range("seer_window_prefill");
+  SEER_TRY(check_dims(d));
+  if (a == nullptr || !a->seqlens) return SEER_ERR_INVALID_ARG;
+  if (a->total_tokens < 0 || a->max_new < 1) return SEER_ERR_INVALID_ARG;
+  if (a->total_tokens > 0 && (!a->q || !a->out)) return SEER_ERR_INVALID_ARG;
+  if (a->cu_tokens == nullptr && (a->total_tokens != d->batch || a->max_new != 1))
+    return SEER_ERR_INVALID_ARG;
+  if (a->window < 1 || a->sinks < 0) return SEER_ERR_INVALID_ARG;
+  if (!(a->softmax_scale > 0.f) || !(a->softmax_scale < INFINITY)) return SEER_ERR_INVALID_ARG;
+  SEER_TRY(check_cache(d, SEER_CACHE_BF16, a->k_pool, a->v_pool, nullptr, nullptr));
+  if (!aligned(a->q, 16) || !aligned(a->out, 16)) return SEER_ERR_UNSUPPORTED;
+  if (a->total_tokens == 0) return SEER_OK;
+  WindowPrefillParams p = {};
+  p.cu = a->cu_tokens;
+  p.seqlens = a->seqlens;
+  p.page_table = a->page_table;
+  p.out = a->out;
+  p.lse = a->lse_out;
+  p.status = a->dev_status;
+  p.B = d->batch;
+  p.Hq = d->num_q_heads;
+  p.Hkv = d->num_kv_heads;
+  p.G = d->num_q_heads / d->num_kv_heads;
+  p.bs = d->block_size;
+  p.max_blocks = d->max_blocks;
+  p.T = a->total_tokens;
+  p.max_new = a->max_new;
+  p.window = a->window;
+  p.sinks = a->sinks;
+  p.ntok = kWPTileRows / p.G;
+  p.token_inner = d->stride_token < d->stride_head ? 1 : 0;
+  p.num_pages = d->num_pages;
+  p.scale_log2 = a->softmax_scale * kLog2e;
+  CUtensorMap tq, tk, tv;
+  SEER_TRY(make_rows_map(a->q, d, p.T, p.ntok, &tq));
+  SEER_TRY(make_kv_map(a->k_pool, d, p.token_inner, &tk));
+  SEER_TRY(make_kv_map(a->v_pool, d, p.token_inner, &tv));
+  SEER_CUDA(run_window_prefill(tq, tk, tv, p, stream));
   return SEER_OK;
 }
 

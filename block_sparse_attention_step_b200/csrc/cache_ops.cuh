@@ -57,6 +57,24 @@ struct CacheDecodeParams {
   float scale_log2;
 };
 
+// Sliding-window attention of a ragged chunk of query tokens.
+struct WindowPrefillParams {
+  const int32_t* cu;  // [B + 1], or nullptr: one token per sequence
+  const int32_t* seqlens;
+  const int32_t* page_table;
+  uint16_t* out;  // [T][Hq][D]
+  float* lse;     // optional [Hq][T]
+  int32_t* status;
+  int B, Hq, Hkv, G, bs, max_blocks, T, max_new, window, sinks;
+  int ntok;  // query tokens of a 128-row tile, floor(128 / G)
+  int token_inner;
+  int64_t num_pages;
+  float scale_log2;
+};
+
+cudaError_t run_window_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const WindowPrefillParams& p, cudaStream_t stream);
+
 cudaError_t run_cache_decode(const CUtensorMap& tk, const CUtensorMap& tv,
                              const CacheDecodeParams& p, int cache, bool window,
                              cudaStream_t stream);

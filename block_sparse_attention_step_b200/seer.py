@@ -49,7 +49,7 @@ EXPORTS = (
     "seer_block_lse_elems", "seer_sparse_decode_mass", "seer_block_mass",
     "seer_rope_table", "seer_append_rope",
     "seer_sparse_decode_q8_splits", "seer_window_decode_splits", "seer_split_workspace_bytes",
-    "seer_sparse_decode_q8", "seer_window_decode",
+    "seer_sparse_decode_q8", "seer_window_decode", "seer_window_prefill",
 )
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -126,6 +126,16 @@ class seer_cache_attn_args(ctypes.Structure):
                 ("lse_out", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
 
 
+class seer_window_prefill_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+                ("cu_tokens", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seqlens", ctypes.c_void_p), ("total_tokens", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("lse_out", ctypes.c_void_p),
+                ("dev_status", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(seer_dims)
 _I = ctypes.c_int32
@@ -167,6 +177,7 @@ _SIGS = {
     "seer_split_workspace_bytes": (ctypes.c_size_t, [_D, _I]),
     "seer_sparse_decode_q8": (_I, [_D, ctypes.POINTER(seer_cache_attn_args), _P]),
     "seer_window_decode": (_I, [_D, ctypes.POINTER(seer_cache_attn_args), _P]),
+    "seer_window_prefill": (_I, [_D, ctypes.POINTER(seer_window_prefill_args), _P]),
 }
 
 _lib_handle = None
@@ -643,3 +654,31 @@ def seer_sparse_decode_q8(d, args: seer_cache_attn_args, stream=None):
 def seer_window_decode(d, args: seer_cache_attn_args, stream=None):
     """Sliding-window decode attention with sink tokens, out and lse in one call."""
     _call("seer_window_decode", d, args, stream)
+
+
+def window_prefill_args(q, k_pool, v_pool, page_table, seqlens, *, window, sinks, softmax_scale,
+                        out, cu_tokens=None, max_new=1, lse_out=None,
+                        dev_status=None) -> seer_window_prefill_args:
+    """Arguments of seer_window_prefill: q and out [T][Hq][D] bf16, lse_out
+    [Hq][T] fp32, bfloat16 pools."""
+    a = seer_window_prefill_args()
+    a.q = _ptr(q, torch.bfloat16, "q")
+    a.k_pool = _ptr(k_pool, torch.bfloat16, "k_pool")
+    a.v_pool = _ptr(v_pool, torch.bfloat16, "v_pool")
+    a.cu_tokens = _ptr(cu_tokens, torch.int32, "cu_tokens", allow_none=True)
+    a.page_table = _ptr(page_table, torch.int32, "page_table", allow_none=True)
+    a.seqlens = _ptr(seqlens, torch.int32, "seqlens")
+    a.total_tokens = q.shape[0]
+    a.max_new = int(max_new)
+    a.window = int(window)
+    a.sinks = int(sinks)
+    a.softmax_scale = float(softmax_scale)
+    a.out = _ptr(out, torch.bfloat16, "out")
+    a.lse_out = _ptr(lse_out, torch.float32, "lse_out", allow_none=True)
+    a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
+    return _keep(a, q, k_pool, v_pool, cu_tokens, page_table, seqlens, out, lse_out, dev_status)
+
+
+def seer_window_prefill(d, args: seer_window_prefill_args, stream=None):
+    """Sliding-window attention with sink tokens for a ragged chunk of query tokens."""
+    _call("seer_window_prefill", d, args, stream)

@@ -608,6 +608,36 @@ SEER_API seer_status seer_sparse_decode_q8(const seer_dims *d, const seer_cache_
 SEER_API seer_status seer_window_decode(const seer_dims *d, const seer_cache_attn_args *a,
                                         seer_stream stream);
 
+/* Sliding-window attention with sinks for a ragged chunk of query tokens (a
+ * prompt, chunks of prompts behind a context, or single tokens), over a bf16
+ * cache that already holds their keys and values (seer_append_rope with the
+ * same cu_tokens and seqlens): the query at position p sees the tokens t <= p
+ * with t > p - window or t < sinks.  cu_tokens, total_tokens, max_new and the
+ * sequences that are left out are those of seer_append_rope; rows that belong
+ * to no sequence keep what out and lse hold.  Blocks that no query of the call
+ * sees are not looked up.  softmax_scale > 0.  A NaN or inf in the value row of
+ * a token that some of the neighbouring queries see reaches those neighbours
+ * too (2 * floor(128 / group) query tokens are worked on together). */
+typedef struct seer_window_prefill_args {
+  const uint16_t *q;         /* [T][Hq][D] bf16, 16-byte aligned */
+  const uint16_t *k_pool;
+  const uint16_t *v_pool;
+  const int32_t *cu_tokens;  /* [B + 1], or NULL */
+  const int32_t *page_table; /* may be NULL (identity) */
+  const int32_t *seqlens;
+  int32_t total_tokens;      /* T */
+  int32_t max_new;
+  int32_t window;            /* >= 1 */
+  int32_t sinks;             /* >= 0 */
+  float softmax_scale;
+  uint16_t *out;             /* [T][Hq][D] bf16, 16-byte aligned */
+  float *lse_out;            /* [Hq][T], may be NULL */
+  int32_t *dev_status;       /* may be NULL */
+} seer_window_prefill_args;
+
+SEER_API seer_status seer_window_prefill(const seer_dims *d, const seer_window_prefill_args *a,
+                                         seer_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
