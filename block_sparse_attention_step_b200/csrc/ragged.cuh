@@ -7,6 +7,18 @@
 
 namespace seer {
 
+// True in one lane of a converged warp.  Code under it is known to run in a
+// single thread, so the operands of tensor-core and TMA instructions stay in
+// uniform registers; under `lane == 0` the compiler issues each of them through
+// a loop over the active lanes (180 cycles per tcgen05.mma instead of the 64
+// that a 128 x 128 x 16 one takes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
 struct Seq {
   int first, n, L;  // rows first .. first + n - 1 are its new tokens
 };

@@ -16,7 +16,7 @@
 //     tensor memory); after P_i V_j it issues S_i for tile j + 1 at once (MMAs
 //     of one thread execute in order, so S may overwrite P), and tile 1's MMAs
 //     run while tile 0's softmax does and the other way round;
-//   * warp 2 zeroes the V rows of tokens no row of the CTA sees (a zero weight
+//   * warps 2 and 3 zero the V rows of tokens no row of the CTA sees (a zero weight
 //     times a cached NaN would be NaN);
 //   * warps 4-7 and 8-11, one row per thread: read S from tensor memory (half 0
 //     for its maximum, half 1 kept, half 0 again), exponentiate in the exp2
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kWPThreads, 1)
   uint8_t* v_ring = k_ring + kWPStages * kWPTile;
   __shared__ WPBars bars;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int h = (int)blockIdx.x % p.Hkv;
   const int item = (int)blockIdx.x / p.Hkv;
   const int per_cta = 2 * p.ntok;
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kWPThreads, 1)
         mbar_init(&bars.k_full[s], 1);
         mbar_init(&bars.k_empty[s], 1);
         mbar_init(&bars.v_full[s], 1);
-        mbar_init(&bars.v_fixed[s], 1);
+        mbar_init(&bars.v_fixed[s], 2);
         mbar_init(&bars.v_empty[s], 1);
       }
       for (int i = 0; i < 2; ++i) {
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kWPThreads, 1)
 
   if (warp == 0) {
     // ================================================================ copies
-    if (lane == 0 && nt > 0) {
+    if (nt > 0 && elect_one()) {
       prefetch_tensormap(&tm_q);
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kWPThreads, 1)
     }
   } else if (warp == 1) {
     // ================================================================ MMA
-    if (lane == 0 && nt > 0) {
+    if (nt > 0 && elect_one()) {
       bool ok = mbar_wait(&bars.q_full, 0);
       const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
       const int tiles = two ? 2 : 1;
@@ -323,8 +323,10 @@ __global__ void __launch_bounds__(kWPThreads, 1)
       tc_commit(&bars.mma_done);
       if (!mbar_wait(&bars.mma_done, 0)) flag_status(p.status, SEER_DEV_TIMEOUT);
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
     // ========================================= V rows that no row sees: zero
+    // (tokens between the sinks and the first window, and past the last query)
+    const int tid = threadIdx.x - 64;
     for (int it = 0; it < nt; ++it) {
       const int s0 = keys.base(it), st = it % kWPStages;
       // every tile is waited for in turn (a parity wait cannot tell a phase
@@ -335,13 +337,13 @@ __global__ void __launch_bounds__(kWPThreads, 1)
         break;
       }
       if (!keys.covered(s0, kWPKeys)) {
-        uint8_t* vd = v_ring + st * kWPTile;
-        for (int i = lane; i < kWPKeys * 16; i += 32) {
-          const int key = i >> 4, piece = i & 15;
-          if (!keys.seen(s0 + key))
-            *reinterpret_cast<uint4*>(vd + (piece >> 3) * kWPHalf + key * 128 + (piece & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
+        uint8_t* vd = v_ring + st * kWPTile + (tid & 7) * 16 + ((tid >> 3) & 1) * kWPHalf;
+        auto zero = [&](int lo, int hi) {  // 64 threads: 4 rows of 16 pieces at a time
+          for (int key = lo + (tid >> 4); key < hi; key += 4)
+            *reinterpret_cast<uint4*>(vd + key * 128) = make_uint4(0u, 0u, 0u, 0u);
+        };
+        zero(max(0, keys.sinks - s0), min(kWPKeys, keys.p_min - p.window + 1 - s0));
+        zero(max(0, keys.p_max + 1 - s0), kWPKeys);
         fence_proxy_async_smem();
         __syncwarp();
       }
