@@ -41,6 +41,10 @@ constexpr int kWPStages = 2;
 constexpr size_t kWPData = (size_t)(2 + 2 * kWPStages) * kWPTile;  // 192 KB
 constexpr size_t kWPSmem = 1024 + kWPData;
 constexpr float kWPSlack = 8.f;
+#ifndef WP_POLY
+#define WP_POLY 4
+#endif
+constexpr int kWPPolyEvery = WP_POLY;  // one pair in so many takes the FMA pipe's 2^y
 constexpr uint32_t kWPIdescS = tc_idesc_bf16(kWPRows, kWPKeys, 0, 0);
 constexpr uint32_t kWPIdescPV = tc_idesc_bf16(kWPRows, kHeadDim, 0, 1);
 
@@ -48,7 +52,7 @@ struct WPBars {
   uint64_t q_full;
   uint64_t k_full[kWPStages], k_empty[kWPStages];
   uint64_t v_full[kWPStages], v_fixed[kWPStages], v_empty[kWPStages];
-  uint64_t s_full[2], p_ready[2][2], pv_done[2];
+  uint64_t s_full[2], p_ready[2][2], pv_half[2], pv_done[2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int b, tile;
@@ -73,6 +77,64 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
       "l"(policy)
       : "memory");
+}
+
+// Packed fp32 pairs.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 2^y of a pair, y <= 8, on the FMA pipe: y = n + f with n its nearest integer,
+// 2^f by the degree-5 polynomial of least relative error on [-1/2, 1/2] (Remez
+// exchange; 2.3e-7 in fp32), times 2^n.  y below -126 gives 2^-126, NaN gives
+// NaN.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t y2) {
+  float a, b;
+  unpack2(y2, a, b);
+  y2 = pack2(max_nan(a, -126.f), max_nan(b, -126.f));
+  const uint64_t magic = pack2(12582912.f, 12582912.f), unmagic = pack2(-12582912.f, -12582912.f);
+  const uint64_t t2 = add2(y2, magic);
+  const uint64_t f2 = fma2(add2(t2, unmagic), pack2(-1.f, -1.f), y2);
+  uint64_t r = pack2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
+  r = fma2(r, f2, pack2(9.675540961325169e-3f, 9.675540961325169e-3f));
+  r = fma2(r, f2, pack2(5.550713092088699e-2f, 5.550713092088699e-2f));
+  r = fma2(r, f2, pack2(2.4022120237350464e-1f, 2.4022120237350464e-1f));
+  r = fma2(r, f2, pack2(6.931469440460205e-1f, 6.931469440460205e-1f));
+  r = fma2(r, f2, pack2(1.0000001192092896f, 1.0000001192092896f));
+  float ta, tb;
+  unpack2(t2, ta, tb);
+  return mul2(r, pack2(__uint_as_float((__float_as_uint(ta) << 23) + 0x3f800000u),
+                       __uint_as_float((__float_as_uint(tb) << 23) + 0x3f800000u)));
+}
+
+// The lowest n of 64 bits (n clamped to 0 .. 64).
+__device__ __forceinline__ uint64_t below(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
 }
 
 // The key tiles of a CTA whose rows lie at positions p_min .. p_max.
@@ -127,7 +189,9 @@ __global__ void __launch_bounds__(kWPThreads, 1)
   const int item = (int)blockIdx.x / p.Hkv;
   const int per_cta = 2 * p.ntok;
 
-  // ---- which sequence and which of its token tiles (warp 0)
+  // ---- which sequence and which of its token tiles (warp 0); meanwhile
+  // tensor memory (warp 1), barriers (warp 2), tensor maps (warp 3)
+  __shared__ int stop;
   if (warp == 0) {
     int passed = 0, found_b = -1, found_tile = 0;
     Seq found = {0, 0, 0};
@@ -158,6 +222,12 @@ __global__ void __launch_bounds__(kWPThreads, 1)
       bars.b = found_b;
       bars.tile = found_tile;
       bars.seq = found;
+    }
+  } else if (warp == 1) {
+    tmem_alloc(&bars.tmem_base, 512);
+    tmem_relinquish_alloc_permit();
+  } else if (warp == 2) {
+    if (lane == 0) {
       mbar_init(&bars.q_full, 1);
       for (int s = 0; s < kWPStages; ++s) {
         mbar_init(&bars.k_full[s], 1);
@@ -170,29 +240,32 @@ __global__ void __launch_bounds__(kWPThreads, 1)
         mbar_init(&bars.s_full[i], 1);
         mbar_init(&bars.p_ready[i][0], 4);
         mbar_init(&bars.p_ready[i][1], 4);
+        mbar_init(&bars.pv_half[i], 1);
         mbar_init(&bars.pv_done[i], 1);
       }
       mbar_init(&bars.mma_done, 1);
       fence_mbar_init();
     }
-  }
-  __syncthreads();
-  const int b = bars.b;
-  if (b < 0) return;  // past the last tile: the whole CTA
-  // after a wait has run out somewhere in the grid, later CTAs do no work
-  // (each run-out wait costs about a second); one thread decides for all
-  __shared__ int stop;
-  if (threadIdx.x == 0)
-    stop = p.status != nullptr &&
-           (*reinterpret_cast<const volatile int32_t*>(p.status) & SEER_DEV_TIMEOUT);
-  if (warp == 1) {
-    tmem_alloc(&bars.tmem_base, 512);
-    tmem_relinquish_alloc_permit();
+  } else if (warp == 3) {
+    if (lane == 0) {
+      prefetch_tensormap(&tm_q);
+      prefetch_tensormap(&tm_k);
+      prefetch_tensormap(&tm_v);
+      // after a wait has run out somewhere in the grid, later CTAs do no work
+      // (each run-out wait costs about a second); one thread decides for all
+      stop = p.status != nullptr &&
+             (*reinterpret_cast<const volatile int32_t*>(p.status) & SEER_DEV_TIMEOUT);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  if (bars.b < 0) {  // past the last tile: the whole CTA
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int b = bars.b;
   const Seq seq = bars.seq;
   const int past = seq.L - seq.n;
   const int t0 = bars.tile * per_cta;                      // first query token of the CTA
@@ -204,9 +277,6 @@ __global__ void __launch_bounds__(kWPThreads, 1)
   if (warp == 0) {
     // ================================================================ copies
     if (nt > 0 && elect_one()) {
-      prefetch_tensormap(&tm_q);
-      prefetch_tensormap(&tm_k);
-      prefetch_tensormap(&tm_v);
       const uint64_t q_policy = policy_evict_first();
       const uint64_t policy = policy_evict_normal();
       const int tiles = two ? 2 : 1;
@@ -304,6 +374,7 @@ __global__ void __launch_bounds__(kWPThreads, 1)
               tc_mma_f16_ts(tmem + 256 + 128 * i, pa + 8 * kk,
                             tc_desc_sw128(va + 2048 * kk, kWPHalf, 1024), kWPIdescPV,
                             (it > 0 || half == 0 || kk > 0) ? 1u : 0u);
+            if (half == 1) tc_commit(&bars.pv_half[i]);
           }
           if (!ok) break;
           if (it == nt - 1) tc_commit(&bars.pv_done[i]);
@@ -373,73 +444,84 @@ __global__ void __launch_bounds__(kWPThreads, 1)
         const bool whole = s0 + kWPKeys - 1 <= pa && (s0 > pz - p.window || s0 + kWPKeys <= p.sinks);
         // this row's keys c of the tile: c < hi and (c >= lo or c < sk)
         const int hi = live ? pos - s0 + 1 : 0, lo = pos - p.window + 1 - s0, sk = p.sinks - s0;
-        uint32_t x[64];
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 1; half >= 0; --half) {
+          uint32_t x[64];
           __syncwarp();
           tmem_ld64(s_addr + 64 * half, x);
           if (!whole) {
+            const uint64_t seen = below(hi - 64 * half) & (~below(lo - 64 * half) | below(sk - 64 * half));
+            const uint32_t w[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const int k = c + 64 * half;
-              if (!(k < hi && (k >= lo || k < sk))) x[c] = 0xff800000u;
+            for (int c = 0; c < 64; ++c)
+              if (!(w[c >> 5] & (1u << (c & 31)))) x[c] = 0xff800000u;
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 64; c += 2)
+            m4[(c >> 1) & 3] = fmaxf(m4[(c >> 1) & 3],
+                                     fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          const bool over = mx > m_ref + kWPSlack;
+          if (__any_sync(0xffffffffu, over)) {
+            float alpha = 1.f;
+            if (over) {
+              if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - mx);
+              m_ref = mx;
             }
-          }
-#pragma unroll
-          for (int c = 0; c < 64; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(x[c]));
-        }
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-        float alpha = 1.f;
-        bool rescale = false;
-        if (mx > m_ref + kWPSlack) {
-          if (m_ref != -INFINITY) {
-            alpha = fast_exp2(m_ref - mx);
-            rescale = true;
-          }
-          m_ref = mx;
-        }
-        if (__any_sync(0xffffffffu, rescale)) {
-          // O is stable: the previous tile's P V was issued before this tile's S
+            l *= alpha;
+            // O holds the tiles before this one (their P V was issued before
+            // this tile's S) and, at half 0, this tile's half 1
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+              if (half == 0) {
+                ok = mbar_wait(&bars.pv_half[i], it & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+              }
 #pragma unroll 1
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t o[32];
-            __syncwarp();
-            tmem_ld32(o_addr + 32 * c4, o);
+              for (int c4 = 0; c4 < 4; ++c4) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(o_addr + 32 * c4, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            __syncwarp();
-            tmem_st32(o_addr + 32 * c4, o);
-          }
-        }
-        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int half = 1; half >= 0; --half) {
-          if (half == 0) {
-            __syncwarp();
-            tmem_ld64(s_addr, x);
-            if (!whole) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (!(c < hi && (c >= lo || c < sk))) x[c] = 0xff800000u;
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                __syncwarp();
+                tmem_st32(o_addr + 32 * c4, o);
+              }
             }
           }
+          const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+          const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), ref2 = pack2(-ref, -ref);
+          uint64_t sum2[2] = {0, 0};
           uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float a = fast_exp2(fmaf(__uint_as_float(x[c]), p.scale_log2, -ref));
-            const float e = fast_exp2(fmaf(__uint_as_float(x[c + 1]), p.scale_log2, -ref));
-            s4[(c >> 1) & 3] += a + e;
-            pk[c >> 1] = pack_bf16x2(a, e);
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t y2 = fma2(pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])),
+                                     scale2, ref2);
+            uint64_t e2;
+            if (c % kWPPolyEvery == kWPPolyEvery - 1) {
+              e2 = exp2_poly2(y2);
+            } else {
+              float a, e;
+              unpack2(y2, a, e);
+              e2 = pack2(fast_exp2(a), fast_exp2(e));
+            }
+            sum2[c & 1] = add2(sum2[c & 1], e2);
+            float a, e;
+            unpack2(e2, a, e);
+            pk[c] = pack_bf16x2(a, e);
           }
           __syncwarp();
           tmem_st32(s_addr + 64 * half, pk);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.p_ready[i][half]);
+          float a, e;
+          unpack2(add2(sum2[0], sum2[1]), a, e);
+          l += a + e;
         }
-        l = l * alpha + ((s4[0] + s4[1]) + (s4[2] + s4[3]));
+        if (!ok) break;
       }
       if (!ok) flag_status(p.status, SEER_DEV_TIMEOUT);
       // ---- epilogue: the last P V, then normalise, bf16 out, natural-log lse
@@ -451,25 +533,36 @@ __global__ void __launch_bounds__(kWPThreads, 1)
       }
       tc_fence_after();
       if (have) {
+        // rows through shared memory (this tile's q, which no MMA reads any
+        // more), so that a row leaves as one 256-byte piece
         const int qh = h * p.G + r % p.G;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* orow = p.out + ((int64_t)(seq.first + tok) * p.Hq + qh) * kHeadDim;
+        uint8_t* stage = q_s + i * kWPTile;
 #pragma unroll 1
         for (int c2 = 0; c2 < 2; ++c2) {
           uint32_t o[64];
           __syncwarp();
           tmem_ld64(o_addr + 64 * c2, o);
-          if (live) {
 #pragma unroll
-            for (int e8 = 0; e8 < 8; ++e8) {
-              uint4 v;
-              v.x = pack_bf16x2(__uint_as_float(o[8 * e8 + 0]) * inv, __uint_as_float(o[8 * e8 + 1]) * inv);
-              v.y = pack_bf16x2(__uint_as_float(o[8 * e8 + 2]) * inv, __uint_as_float(o[8 * e8 + 3]) * inv);
-              v.z = pack_bf16x2(__uint_as_float(o[8 * e8 + 4]) * inv, __uint_as_float(o[8 * e8 + 5]) * inv);
-              v.w = pack_bf16x2(__uint_as_float(o[8 * e8 + 6]) * inv, __uint_as_float(o[8 * e8 + 7]) * inv);
-              *reinterpret_cast<uint4*>(orow + 64 * c2 + 8 * e8) = v;
-            }
+          for (int e8 = 0; e8 < 8; ++e8) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(o[8 * e8 + 0]) * inv, __uint_as_float(o[8 * e8 + 1]) * inv);
+            v.y = pack_bf16x2(__uint_as_float(o[8 * e8 + 2]) * inv, __uint_as_float(o[8 * e8 + 3]) * inv);
+            v.z = pack_bf16x2(__uint_as_float(o[8 * e8 + 4]) * inv, __uint_as_float(o[8 * e8 + 5]) * inv);
+            v.w = pack_bf16x2(__uint_as_float(o[8 * e8 + 6]) * inv, __uint_as_float(o[8 * e8 + 7]) * inv);
+            *reinterpret_cast<uint4*>(stage + r * 256 + (((8 * c2 + e8) ^ (r & 15)) << 4)) = v;
           }
+        }
+        __syncwarp();
+        const int r0 = 32 * (warp & 3) + (lane >> 4), piece = lane & 15;
+#pragma unroll 4
+        for (int k = 0; k < 16; ++k) {
+          const int rr = r0 + 2 * k, tk = rr / p.G, g = rr - tk * p.G;
+          const int t = t0 + i * p.ntok + tk;
+          if (tk < p.ntok && t < seq.n)
+            *reinterpret_cast<uint4*>(p.out + ((int64_t)(seq.first + t) * p.Hq + h * p.G + g) * kHeadDim +
+                                      8 * piece) =
+                *reinterpret_cast<const uint4*>(stage + rr * 256 + ((piece ^ (rr & 15)) << 4));
         }
         if (live && p.lse != nullptr)
           p.lse[(int64_t)qh * p.T + seq.first + tok] =
