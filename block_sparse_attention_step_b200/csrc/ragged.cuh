@@ -19,6 +19,30 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// mbar_wait for kernels whose warps wait most of the time next to others that
+// are short of issue slots: no suspend-time hint, so the hardware holds the
+// warp until the phase completes or its own time limit passes (with a hint
+// the wait becomes a loop of polls and short sleeps: a third of all
+// instructions of the prefill).  Bounded like mbar_wait.
+__device__ __forceinline__ bool mbar_hold(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    const long long now = clock64();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > (1ll << 31)) return false;
+  }
+}
+
 struct Seq {
   int first, n, L;  // rows first .. first + n - 1 are its new tokens
 };
