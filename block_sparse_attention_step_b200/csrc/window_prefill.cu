@@ -54,7 +54,7 @@ struct WPBars {
   uint64_t q_full;
   uint64_t k_full[kWPKStages], k_empty[kWPKStages];
   uint64_t v_full[kWPVStages], v_fixed[kWPVStages], v_empty[kWPVStages];
-  uint64_t s_full[2], p_ready, pv_done[2];
+  uint64_t s_full[2], p_ready[2], pv_done[2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int b, tile, stop;
@@ -240,9 +240,11 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bars.s_full[i], 1);
+        // one per S buffer: a warp may be a tile ahead of another, and its
+        // arrival must not count for the other's tile
+        mbar_init(&bars.p_ready[i], 4);
         mbar_init(&bars.pv_done[i], 1);
       }
-      mbar_init(&bars.p_ready, 4);
       mbar_init(&bars.mma_done, 1);
       fence_mbar_init();
     }
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
         const int vs = it % kWPVStages;
         const uint32_t ph = (it / kWPVStages) & 1;
         if (!mbar_hold(&bars.v_full[vs], ph) || !mbar_hold(&bars.v_fixed[vs], ph) ||
-            !mbar_hold(&bars.p_ready, it & 1)) {
+            !mbar_hold(&bars.p_ready[it & 1], (it >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       tmem_st32(s_addr, pk);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_ready);
+      if (lane == 0) mbar_arrive(&bars.p_ready[it & 1]);
       float a, e;
       unpack2(add2(sum2[0], sum2[1]), a, e);
       l += a + e;
