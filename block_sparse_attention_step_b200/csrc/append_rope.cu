@@ -23,9 +23,10 @@
 //
 // Two roles share one grid:
 //   * block role, one CTA per (touched block, KV head): the block's new rows of
-//     k and v stay in registers between the amax and the rounding, so they are
-//     read once; the block's keys meet in shared memory for the pooled key
-//     (the mean of the rows as the cache holds them, summed in the order of
+//     k and v come into shared memory by asynchronous copies, all in flight at
+//     once, and stay on the SM between the amax and the rounding, so they are
+//     read once; the block's keys as the cache gets them replace the raw ones
+//     there, for the pooled key (their mean, summed in the order of
 //     block_mean.cuh).  Needed for an 8-bit cache and for pooled keys.
 //   * row role, a tile of tokens per CTA: q rows, and k and v rows too when the
 //     cache is bf16 and no pooled keys are wanted.
@@ -43,6 +44,7 @@ namespace seer {
 constexpr int kRowThreads = 8;      // threads per 128-dim row
 constexpr int kRowTileRows = 128;   // rows of a row-role tile, about
 constexpr int kMaxTileTokens = 128;
+constexpr int kRowsInFlight = 2;    // rows a thread of the row role reads at once
 
 // ------------------------------------------------------------- 8-bit codes
 template <int CACHE>
@@ -269,47 +271,69 @@ __device__ __forceinline__ void row_role(const AppendParams& p, int tile, RowSha
   const int hq = p.q != nullptr ? p.Hq : 0;
   const int R = hq + (p.rows_kv ? 2 * p.Hkv : 0);
   const Slot sl = slot_of(p, tid % kRowThreads);
-  for (int r = tid / kRowThreads; r < ntok * R; r += nthr / kRowThreads) {
-    const int i = r / R;
-    int h = r - i * R;
-    if (sh.rope[i] < 0) continue;
-    const int64_t t = t0 + i;
-    const uint16_t* src;
-    uint16_t* dst;
-    bool turned = true;
-    if (h < hq) {
-      src = p.q + t * p.q_stride + (int64_t)h * kHeadDim;
-      dst = p.q_out + t * p.q_out_stride + (int64_t)h * kHeadDim;
-    } else {
-      if (sh.at[i] < 0) continue;
-      h -= hq;
-      const bool is_v = h >= p.Hkv;
-      if (is_v) h -= p.Hkv;
-      src = is_v ? p.v + t * p.v_stride + (int64_t)h * kHeadDim
-                 : p.k + t * p.k_stride + (int64_t)h * kHeadDim;
-      dst = (is_v ? static_cast<uint16_t*>(p.v_pool) : static_cast<uint16_t*>(p.k_pool)) +
-            sh.at[i] + (int64_t)h * p.stride_head;
-      turned = !is_v;
+  const int step = nthr / kRowThreads;
+  // kRowsInFlight rows at a time, all of them read before the first is written
+  for (int r0 = tid / kRowThreads; r0 < ntok * R; r0 += kRowsInFlight * step) {
+    const uint16_t* src[kRowsInFlight];
+    uint16_t* dst[kRowsInFlight];
+    uint4 a[kRowsInFlight], b[kRowsInFlight];
+    int pos[kRowsInFlight];  // table row; -1: not turned
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      const int r = r0 + u * step;
+      src[u] = nullptr;
+      pos[u] = -1;
+      if (r >= ntok * R) continue;
+      const int i = r / R;
+      int h = r - i * R;
+      if (sh.rope[i] < 0) continue;
+      const int64_t t = t0 + i;
+      if (h < hq) {
+        src[u] = p.q + t * p.q_stride + (int64_t)h * kHeadDim;
+        dst[u] = p.q_out + t * p.q_out_stride + (int64_t)h * kHeadDim;
+        pos[u] = sh.rope[i];
+      } else if (sh.at[i] >= 0) {
+        h -= hq;
+        const bool is_v = h >= p.Hkv;
+        if (is_v) h -= p.Hkv;
+        else pos[u] = sh.rope[i];
+        src[u] = is_v ? p.v + t * p.v_stride + (int64_t)h * kHeadDim
+                      : p.k + t * p.k_stride + (int64_t)h * kHeadDim;
+        dst[u] = (is_v ? static_cast<uint16_t*>(p.v_pool) : static_cast<uint16_t*>(p.k_pool)) +
+                 sh.at[i] + (int64_t)h * p.stride_head;
+      }
     }
-    uint4 a = reinterpret_cast<const uint4*>(src)[sl.c0];  // q may be turned in place
-    uint4 b = reinterpret_cast<const uint4*>(src)[sl.c1];
-    if (turned && (sl.turned0 || sl.turned1)) {
-      float x[16];
-      widen8(a, x);
-      widen8(b, x + 8);
-      turn16(p, sl, sh.rope[i], x);
-      a = round8(x);
-      b = round8(x + 8);
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      if (src[u] == nullptr) continue;
+      a[u] = reinterpret_cast<const uint4*>(src[u])[sl.c0];  // q may be turned in place
+      b[u] = reinterpret_cast<const uint4*>(src[u])[sl.c1];
     }
-    reinterpret_cast<uint4*>(dst)[sl.c0] = a;
-    reinterpret_cast<uint4*>(dst)[sl.c1] = b;
+#pragma unroll
+    for (int u = 0; u < kRowsInFlight; ++u) {
+      if (src[u] == nullptr) continue;
+      if (pos[u] >= 0 && (sl.turned0 || sl.turned1)) {
+        float x[16];
+        widen8(a[u], x);
+        widen8(b[u], x + 8);
+        turn16(p, sl, pos[u], x);
+        a[u] = round8(x);
+        b[u] = round8(x + 8);
+      }
+      reinterpret_cast<uint4*>(dst[u])[sl.c0] = a[u];
+      reinterpret_cast<uint4*>(dst[u])[sl.c1] = b[u];
+    }
   }
 }
 
 // ------------------------------------------------------------- block role
 template <int BS>
 struct BlockShared {
-  __align__(16) uint8_t keys[BS * kHeadDim * 2];  // the block's keys as the cache holds them
+  // the block's rows, 16 chunks of 16 bytes each: new rows as they come (bf16),
+  // earlier keys as the cache holds them; a new key's chunk is replaced by what
+  // the cache gets (8-bit codes in the chunk's first half)
+  __align__(16) uint8_t keys[BS * kHeadDim * 2];
+  __align__(16) uint8_t values[BS * kHeadDim * 2];
   __align__(16) float part[kPoolWarps * kHeadDim];
   float red[2][BS / 8];  // one per warp
   int scan[BS / 8];
@@ -317,6 +341,16 @@ struct BlockShared {
   Seq seq;
   float scale[2], shrink[2];
 };
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
 
 // Item number -> (sequence, touched block); false: past the last one.
 template <int BS>
@@ -402,54 +436,67 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
   uint8_t* vp = static_cast<uint8_t*>(p.v_pool) + pool_at * kBytes;
   const int64_t row_bytes = p.stride_token * kBytes;
 
-  // the new rows: g and g + kGroups of the block
-  float x[2][16];
-  uint4 v[2][2];
+  // rows g and g + kGroups of the block, all reads in flight at once; a thread
+  // fetches what it works on itself, so it waits for nobody else
+  uint4* keys = reinterpret_cast<uint4*>(sh.keys);
+  uint4* vals = reinterpret_cast<uint4*>(sh.values);
   bool live[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = g + u * kGroups;
     live[u] = r >= old_rows && r < end;
-    v[u][0] = v[u][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (live[u]) {
+      const int64_t t = s.first + (base + r - past);
+      const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (int64_t)h * kHeadDim);
+      const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (int64_t)h * kHeadDim);
+      cp_async16(keys + r * 16 + sl.c0, ks + sl.c0);
+      cp_async16(keys + r * 16 + sl.c1, ks + sl.c1);
+      cp_async16(vals + r * 16 + sl.c0, vs + sl.c0);
+      cp_async16(vals + r * 16 + sl.c1, vs + sl.c1);
+    } else if (r < old_rows && p.kbar != nullptr) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[u][e] = 0.f;
-    if (!live[u]) continue;
-    const int64_t t = s.first + (base + r - past);
-    const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (int64_t)h * kHeadDim);
-    const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (int64_t)h * kHeadDim);
-    widen8(__ldg(ks + sl.c0), x[u]);
-    widen8(__ldg(ks + sl.c1), x[u] + 8);
-    v[u][0] = __ldg(vs + sl.c0);
-    v[u][1] = __ldg(vs + sl.c1);
+      for (int c = 0; c < 2; ++c) {
+        const int chunk = c ? sl.c1 : sl.c0;
+        if constexpr (kBf16) cp_async16(keys + r * 16 + chunk, kp + r * row_bytes + 16 * chunk);
+        else cp_async8(keys + r * 16 + chunk, kp + r * row_bytes + 8 * chunk);
+      }
+    }
   }
+  float old_scale = 0.f;
+  if constexpr (!kBf16) {
+    if (tid < 2 && old_rows > 0) old_scale = (tid == 0 ? p.k_scale : p.v_scale)[page * p.Hkv + h];
+  }
+  cp_async_wait();
+
+  float x[2][16];  // the new keys, turned
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    if (live[u] && (sl.turned0 || sl.turned1)) {
-      const int r = g + u * kGroups;
-      turn16(p, sl, rope_row(p, s.first + (base + r - past), base + r), x[u]);
+    const int r = g + u * kGroups;
+    if (live[u]) {
+      widen8(keys[r * 16 + sl.c0], x[u]);
+      widen8(keys[r * 16 + sl.c1], x[u] + 8);
+      if (sl.turned0 || sl.turned1)
+        turn16(p, sl, rope_row(p, s.first + (base + r - past), base + r), x[u]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[u][e] = 0.f;
     }
   }
 
   if constexpr (kBf16) {
-    uint4* keys = reinterpret_cast<uint4*>(sh.keys);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = g + u * kGroups;
-      if (live[u]) {
-        const uint4 a = round8(x[u]), c = round8(x[u] + 8);
-        uint4* kd = reinterpret_cast<uint4*>(kp + r * row_bytes);
-        uint4* vd = reinterpret_cast<uint4*>(vp + r * row_bytes);
-        kd[sl.c0] = a;
-        kd[sl.c1] = c;
-        vd[sl.c0] = v[u][0];
-        vd[sl.c1] = v[u][1];
-        keys[r * 16 + sl.c0] = a;
-        keys[r * 16 + sl.c1] = c;
-      } else if (r < old_rows) {
-        const uint4* kd = reinterpret_cast<const uint4*>(kp + r * row_bytes);
-        keys[r * 16 + sl.c0] = kd[sl.c0];
-        keys[r * 16 + sl.c1] = kd[sl.c1];
-      }
+      if (!live[u]) continue;
+      const uint4 a = round8(x[u]), c = round8(x[u] + 8);
+      uint4* kd = reinterpret_cast<uint4*>(kp + r * row_bytes);
+      uint4* vd = reinterpret_cast<uint4*>(vp + r * row_bytes);
+      kd[sl.c0] = a;
+      kd[sl.c1] = c;
+      vd[sl.c0] = vals[r * 16 + sl.c0];
+      vd[sl.c1] = vals[r * 16 + sl.c1];
+      keys[r * 16 + sl.c0] = a;
+      keys[r * 16 + sl.c1] = c;
     }
   } else {
     // largest finite magnitudes of the new rows
@@ -457,9 +504,11 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
     bool fine = true;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      if (!live[u]) continue;
+      const int r = g + u * kGroups;
       float y[16];
-      widen8(v[u][0], y);
-      widen8(v[u][1], y + 8);
+      widen8(vals[r * 16 + sl.c0], y);
+      widen8(vals[r * 16 + sl.c1], y + 8);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const float a = fabsf(x[u][e]), c = fabsf(y[e]);
@@ -483,11 +532,10 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
     if (tid < 2) {  // thread 0: k, thread 1: v
       float a = 0.f;
       for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, sh.red[tid][w]);
-      float* sp = (tid == 0 ? p.k_scale : p.v_scale) + page * p.Hkv + h;
-      const float old = old_rows > 0 ? *sp : 0.f;
       float shrink;
-      const float now = grown_scale<CACHE>(old, a, old_rows > 0, &shrink);
-      if (old_rows == 0 || now != old) *sp = now;
+      const float now = grown_scale<CACHE>(old_scale, a, old_rows > 0, &shrink);
+      if (old_rows == 0 || now != old_scale)
+        (tid == 0 ? p.k_scale : p.v_scale)[page * p.Hkv + h] = now;
       sh.scale[tid] = now;
       sh.shrink[tid] = shrink;
     }
@@ -495,59 +543,43 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
     const float inv_k = sh.scale[0] > 0.f ? __frcp_rn(sh.scale[0]) : 0.f;
     const float inv_v = sh.scale[1] > 0.f ? __frcp_rn(sh.scale[1]) : 0.f;
     const float shrink_k = sh.shrink[0], shrink_v = sh.shrink[1];
-    uint2* keys = reinterpret_cast<uint2*>(sh.keys);  // [BS][16] chunks of 8 codes
+    auto code8 = [](const float* y, float f) {
+      return make_uint2(
+          Code8<CACHE>::pack4(__fmul_rn(y[0], f), __fmul_rn(y[1], f), __fmul_rn(y[2], f),
+                              __fmul_rn(y[3], f)),
+          Code8<CACHE>::pack4(__fmul_rn(y[4], f), __fmul_rn(y[5], f), __fmul_rn(y[6], f),
+                              __fmul_rn(y[7], f)));
+    };
+    auto recode = [&](uint2 w, float f) {
+      float y[8];
+      Code8<CACHE>::unpack4(w.x, *reinterpret_cast<float(*)[4]>(y));
+      Code8<CACHE>::unpack4(w.y, *reinterpret_cast<float(*)[4]>(y + 4));
+      return code8(y, f);
+    };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int r = g + u * kGroups;
       uint2* kd = reinterpret_cast<uint2*>(kp + r * row_bytes);
       uint2* vd = reinterpret_cast<uint2*>(vp + r * row_bytes);
-      if (live[u]) {
-        float y[16];
-        widen8(v[u][0], y);
-        widen8(v[u][1], y + 8);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float* xk = x[u] + 8 * c;
-          float* xv = y + 8 * c;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            xk[e] = __fmul_rn(xk[e], inv_k);
-            xv[e] = __fmul_rn(xv[e], inv_v);
-          }
-          const uint2 ck = make_uint2(Code8<CACHE>::pack4(xk[0], xk[1], xk[2], xk[3]),
-                                      Code8<CACHE>::pack4(xk[4], xk[5], xk[6], xk[7]));
-          const int chunk = c ? sl.c1 : sl.c0;
+      for (int c = 0; c < 2; ++c) {
+        const int chunk = c ? sl.c1 : sl.c0;
+        uint2* held = reinterpret_cast<uint2*>(keys + r * 16 + chunk);
+        if (live[u]) {
+          float y[8];
+          widen8(vals[r * 16 + chunk], y);
+          const uint2 ck = code8(x[u] + 8 * c, inv_k);
           kd[chunk] = ck;
-          vd[chunk] = make_uint2(Code8<CACHE>::pack4(xv[0], xv[1], xv[2], xv[3]),
-                                 Code8<CACHE>::pack4(xv[4], xv[5], xv[6], xv[7]));
-          keys[r * 16 + chunk] = ck;
-        }
-      } else if (r < old_rows) {
-        // earlier rows: re-rounded where the scale grew, read for the mean
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int chunk = 2 * i + c;
-          if (shrink_k != 1.f || p.kbar != nullptr) {
-            uint2 w = kd[chunk];
-            if (shrink_k != 1.f) {
-              float y[4], z[4];
-              Code8<CACHE>::unpack4(w.x, y);
-              Code8<CACHE>::unpack4(w.y, z);
-              w.x = Code8<CACHE>::pack4(y[0] * shrink_k, y[1] * shrink_k, y[2] * shrink_k, y[3] * shrink_k);
-              w.y = Code8<CACHE>::pack4(z[0] * shrink_k, z[1] * shrink_k, z[2] * shrink_k, z[3] * shrink_k);
-              kd[chunk] = w;
-            }
-            keys[r * 16 + chunk] = w;
+          vd[chunk] = code8(y, inv_v);
+          *held = ck;
+        } else if (r < old_rows) {
+          // earlier rows: rounded again where the scale grew
+          if (shrink_k != 1.f) {
+            const uint2 w = recode(kd[chunk], shrink_k);
+            kd[chunk] = w;
+            *held = w;
           }
-          if (shrink_v != 1.f) {
-            uint2 w = vd[chunk];
-            float y[4], z[4];
-            Code8<CACHE>::unpack4(w.x, y);
-            Code8<CACHE>::unpack4(w.y, z);
-            w.x = Code8<CACHE>::pack4(y[0] * shrink_v, y[1] * shrink_v, y[2] * shrink_v, y[3] * shrink_v);
-            w.y = Code8<CACHE>::pack4(z[0] * shrink_v, z[1] * shrink_v, z[2] * shrink_v, z[3] * shrink_v);
-            vd[chunk] = w;
-          }
+          if (shrink_v != 1.f) vd[chunk] = recode(vd[chunk], shrink_v);
         }
       }
     }
@@ -572,7 +604,9 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
       a = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int t = warp; t < end; t += kPoolWarps) {
         float y[4];
-        Code8<CACHE>::unpack4(reinterpret_cast<const uint32_t*>(sh.keys)[t * 32 + lane], y);
+        // dims 4 lane .. 4 lane + 3: half of the codes in the first half of chunk lane / 2
+        Code8<CACHE>::unpack4(
+            reinterpret_cast<const uint32_t*>(sh.keys)[t * 64 + (lane >> 1) * 4 + (lane & 1)], y);
         a.x = __fadd_rn(a.x, __fmul_rn(y[0], scale));
         a.y = __fadd_rn(a.y, __fmul_rn(y[1], scale));
         a.z = __fadd_rn(a.z, __fmul_rn(y[2], scale));
@@ -589,20 +623,49 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
 
 // --------------------------------------------------------------- launches
 template <int BS, int CACHE>
-__global__ void __launch_bounds__(BS * 4) append_blocks_kernel(const AppendParams p) {
-  __shared__ union {
-    BlockShared<BS> blk;
-    RowShared row;
-  } sh;
+__global__ void __launch_bounds__(BS * 4, BS == 64 ? 4 : 2) append_blocks_kernel(const AppendParams p) {
+  extern __shared__ __align__(16) uint8_t ap_raw[];
+  pdl_wait();
+  pdl_launch_dependents();
   const int n_blk = p.items * p.Hkv;
   const int c = (int)blockIdx.x;
-  if (c < n_blk) block_role<BS, CACHE>(p, c / p.Hkv, c % p.Hkv, sh.blk);
-  else row_role(p, c - n_blk, sh.row);
+  if (c < n_blk) block_role<BS, CACHE>(p, c / p.Hkv, c % p.Hkv, *reinterpret_cast<BlockShared<BS>*>(ap_raw));
+  else row_role(p, c - n_blk, *reinterpret_cast<RowShared*>(ap_raw));
 }
 
 __global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p) {
   __shared__ RowShared sh;
+  pdl_wait();
+  pdl_launch_dependents();
   row_role(p, (int)blockIdx.x, sh);
+}
+
+template <typename Kernel>
+static cudaError_t launch_append(Kernel kern, const AppendParams& p, int64_t grid, int threads,
+                                 size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <int BS, int CACHE>
+static cudaError_t launch_blocks(const AppendParams& p, int64_t grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> smem_set{0};
+  const cudaError_t e = ensure_smem_limit(append_blocks_kernel<BS, CACHE>, smem_set);
+  if (e != cudaSuccess) return e;
+  static_assert(sizeof(BlockShared<BS>) >= sizeof(RowShared), "both roles share the memory");
+  return launch_append(append_blocks_kernel<BS, CACHE>, p, grid, BS * 4, sizeof(BlockShared<BS>),
+                       stream);
 }
 
 cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream) {
@@ -616,10 +679,7 @@ cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream) {
     if (p.tile_tokens > kMaxTileTokens) p.tile_tokens = kMaxTileTokens;
     tiles = ((int64_t)p.T + p.tile_tokens - 1) / p.tile_tokens;
   }
-  if (p.rows_kv) {
-    append_rows_kernel<<<(unsigned)tiles, 256, 0, stream>>>(p);
-    return cudaGetLastError();
-  }
+  if (p.rows_kv) return launch_append(append_rows_kernel, p, tiles, 256, 0, stream);
   // touched blocks: n tokens from any place in a block reach at most
   // (n + bs - 2) / bs + 1 blocks
   const int64_t per_seq = ((int64_t)p.max_new + p.bs - 2) / p.bs + 1;
@@ -629,17 +689,14 @@ cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream) {
   p.items = (int)items;
   const int64_t grid = items * p.Hkv + tiles;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kern, int threads) { kern<<<(unsigned)grid, threads, 0, stream>>>(p); };
   if (p.bs == 64) {
-    if (cache == SEER_CACHE_BF16) go(append_blocks_kernel<64, SEER_CACHE_BF16>, 256);
-    else if (cache == SEER_CACHE_E4M3) go(append_blocks_kernel<64, SEER_CACHE_E4M3>, 256);
-    else go(append_blocks_kernel<64, SEER_CACHE_INT8>, 256);
-  } else {
-    if (cache == SEER_CACHE_BF16) go(append_blocks_kernel<128, SEER_CACHE_BF16>, 512);
-    else if (cache == SEER_CACHE_E4M3) go(append_blocks_kernel<128, SEER_CACHE_E4M3>, 512);
-    else go(append_blocks_kernel<128, SEER_CACHE_INT8>, 512);
+    if (cache == SEER_CACHE_BF16) return launch_blocks<64, SEER_CACHE_BF16>(p, grid, stream);
+    if (cache == SEER_CACHE_E4M3) return launch_blocks<64, SEER_CACHE_E4M3>(p, grid, stream);
+    return launch_blocks<64, SEER_CACHE_INT8>(p, grid, stream);
   }
-  return cudaGetLastError();
+  if (cache == SEER_CACHE_BF16) return launch_blocks<128, SEER_CACHE_BF16>(p, grid, stream);
+  if (cache == SEER_CACHE_E4M3) return launch_blocks<128, SEER_CACHE_E4M3>(p, grid, stream);
+  return launch_blocks<128, SEER_CACHE_INT8>(p, grid, stream);
 }
 
 // ------------------------------------------------------------------ table
