@@ -42,9 +42,8 @@
 namespace seer {
 
 constexpr int kRowThreads = 8;      // threads per 128-dim row
-constexpr int kRowTileRows = 128;   // rows of a row-role tile, about
+constexpr int kRowTileRows = 384;   // rows of a row-role tile, about
 constexpr int kMaxTileTokens = 128;
-constexpr int kRowsInFlight = 2;    // rows a thread of the row role reads at once
 
 // ------------------------------------------------------------- 8-bit codes
 template <int CACHE>
@@ -174,35 +173,51 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = x;
 }
 
-// A thread's 16 values (chunk c0, then c1) turned by the table row of its
-// token's position.
-__device__ __forceinline__ void turn16(const AppendParams& p, const Slot& s, int pos,
-                                       float (&x)[16]) {
+// A thread's cosines and sines of one table row: halves style, those of pairs
+// (8 c0 + e); interleaved, the four of chunk c0, then the four of chunk c1.
+struct Turn {
+  float4 c[2], w[2];
+};
+
+__device__ __forceinline__ Turn load_turn(const AppendParams& p, const Slot& s, int pos) {
+  Turn t;
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
   const float* row = p.rope + (int64_t)pos * p.rot;
   const int half = p.rot >> 1;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    t.c[k] = one;
+    t.w[k] = zero;
+    if (k ? s.turned1 : s.turned0) {
+      const int at = p.interleaved ? 4 * (k ? s.c1 : s.c0) : 8 * s.c0 + 4 * k;
+      t.c[k] = __ldg(reinterpret_cast<const float4*>(row + at));
+      t.w[k] = __ldg(reinterpret_cast<const float4*>(row + half + at));
+    }
+  }
+  return t;
+}
+
+// A thread's 16 values (chunk c0, then c1), turned.
+__device__ __forceinline__ void turn16(const AppendParams& p, const Slot& s, const Turn& t,
+                                       float (&x)[16]) {
   if (p.interleaved) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k ? s.turned1 : s.turned0) {
-        const int at = 4 * (k ? s.c1 : s.c0);
-        const float4 c = __ldg(reinterpret_cast<const float4*>(row + at));
-        const float4 w = __ldg(reinterpret_cast<const float4*>(row + half + at));
         float* y = x + 8 * k;
-        turn(y[0], y[1], c.x, w.x);
-        turn(y[2], y[3], c.y, w.y);
-        turn(y[4], y[5], c.z, w.z);
-        turn(y[6], y[7], c.w, w.w);
+        turn(y[0], y[1], t.c[k].x, t.w[k].x);
+        turn(y[2], y[3], t.c[k].y, t.w[k].y);
+        turn(y[4], y[5], t.c[k].z, t.w[k].z);
+        turn(y[6], y[7], t.c[k].w, t.w[k].w);
       }
     }
   } else if (s.turned0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + 8 * s.c0 + 4 * k));
-      const float4 w = __ldg(reinterpret_cast<const float4*>(row + half + 8 * s.c0 + 4 * k));
-      turn(x[4 * k], x[8 + 4 * k], c.x, w.x);
-      turn(x[4 * k + 1], x[9 + 4 * k], c.y, w.y);
-      turn(x[4 * k + 2], x[10 + 4 * k], c.z, w.z);
-      turn(x[4 * k + 3], x[11 + 4 * k], c.w, w.w);
+      turn(x[4 * k], x[8 + 4 * k], t.c[k].x, t.w[k].x);
+      turn(x[4 * k + 1], x[9 + 4 * k], t.c[k].y, t.w[k].y);
+      turn(x[4 * k + 2], x[10 + 4 * k], t.c[k].z, t.w[k].z);
+      turn(x[4 * k + 3], x[11 + 4 * k], t.c[k].w, t.w[k].w);
     }
   }
 }
@@ -268,60 +283,60 @@ __device__ __forceinline__ void row_role(const AppendParams& p, int tile, RowSha
     sh.at[i] = at;
   }
   __syncthreads();
+  // A warp takes one token's rows [h0, h1) of q, then k, then v: four rows at a
+  // time with the token's cosines and sines in registers, the next four read
+  // before these are written.
   const int hq = p.q != nullptr ? p.Hq : 0;
-  const int R = hq + (p.rows_kv ? 2 * p.Hkv : 0);
-  const Slot sl = slot_of(p, tid % kRowThreads);
-  const int step = nthr / kRowThreads;
-  // kRowsInFlight rows at a time, all of them read before the first is written
-  for (int r0 = tid / kRowThreads; r0 < ntok * R; r0 += kRowsInFlight * step) {
-    const uint16_t* src[kRowsInFlight];
-    uint16_t* dst[kRowsInFlight];
-    uint4 a[kRowsInFlight], b[kRowsInFlight];
-    int pos[kRowsInFlight];  // table row; -1: not turned
+  const int hk = p.rows_kv ? p.Hkv : 0;
+  const int warp = tid >> 5, lane = tid & 31;
+  const Slot sl = slot_of(p, lane % kRowThreads);
+  const bool any_turned = sl.turned0 || sl.turned1;
+  for (int unit = warp; unit < ntok * p.segments; unit += nthr >> 5) {
+    const int i = unit / p.segments;
+    const int h0 = (unit - i * p.segments) * p.segment_rows, h1 = h0 + p.segment_rows;
+    if (sh.rope[i] < 0) continue;
+    const int64_t t = t0 + i;
+    Turn tn;
+    if (any_turned) tn = load_turn(p, sl, sh.rope[i]);
+    auto rows = [&](const uint16_t* src, uint16_t* dst, int64_t dst_stride, int first, int count,
+                    bool turned) {
+      // rows first .. first + count - 1 of this kind that lie in [h0, h1)
+      const int lo = max(h0 - first, 0), hi = min(h1 - first, count);
+      const int g = lane / kRowThreads;
+      for (int h = lo + g; h < hi; h += 8) {
+        const uint4* s0 = reinterpret_cast<const uint4*>(src + (int64_t)h * kHeadDim);
+        const bool more = h + 4 < hi;
+        uint4 a[2], b[2];
+        a[0] = s0[sl.c0];  // plain loads: q may be turned in place
+        b[0] = s0[sl.c1];
+        if (more) {
+          a[1] = s0[4 * 16 + sl.c0];
+          b[1] = s0[4 * 16 + sl.c1];
+        }
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      const int r = r0 + u * step;
-      src[u] = nullptr;
-      pos[u] = -1;
-      if (r >= ntok * R) continue;
-      const int i = r / R;
-      int h = r - i * R;
-      if (sh.rope[i] < 0) continue;
-      const int64_t t = t0 + i;
-      if (h < hq) {
-        src[u] = p.q + t * p.q_stride + (int64_t)h * kHeadDim;
-        dst[u] = p.q_out + t * p.q_out_stride + (int64_t)h * kHeadDim;
-        pos[u] = sh.rope[i];
-      } else if (sh.at[i] >= 0) {
-        h -= hq;
-        const bool is_v = h >= p.Hkv;
-        if (is_v) h -= p.Hkv;
-        else pos[u] = sh.rope[i];
-        src[u] = is_v ? p.v + t * p.v_stride + (int64_t)h * kHeadDim
-                      : p.k + t * p.k_stride + (int64_t)h * kHeadDim;
-        dst[u] = (is_v ? static_cast<uint16_t*>(p.v_pool) : static_cast<uint16_t*>(p.k_pool)) +
-                 sh.at[i] + (int64_t)h * p.stride_head;
+        for (int u = 0; u < 2; ++u) {
+          if (u == 1 && !more) break;
+          if (turned && any_turned) {
+            float x[16];
+            widen8(a[u], x);
+            widen8(b[u], x + 8);
+            turn16(p, sl, tn, x);
+            a[u] = round8(x);
+            b[u] = round8(x + 8);
+          }
+          uint4* d = reinterpret_cast<uint4*>(dst + (h + 4 * u) * dst_stride);
+          d[sl.c0] = a[u];
+          d[sl.c1] = b[u];
+        }
       }
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      if (src[u] == nullptr) continue;
-      a[u] = reinterpret_cast<const uint4*>(src[u])[sl.c0];  // q may be turned in place
-      b[u] = reinterpret_cast<const uint4*>(src[u])[sl.c1];
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      if (src[u] == nullptr) continue;
-      if (pos[u] >= 0 && (sl.turned0 || sl.turned1)) {
-        float x[16];
-        widen8(a[u], x);
-        widen8(b[u], x + 8);
-        turn16(p, sl, pos[u], x);
-        a[u] = round8(x);
-        b[u] = round8(x + 8);
-      }
-      reinterpret_cast<uint4*>(dst[u])[sl.c0] = a[u];
-      reinterpret_cast<uint4*>(dst[u])[sl.c1] = b[u];
+    };
+    if (h0 < hq)
+      rows(p.q + t * p.q_stride, p.q_out + t * p.q_out_stride, kHeadDim, 0, hq, true);
+    if (h1 > hq && hk > 0 && sh.at[i] >= 0) {
+      rows(p.k + t * p.k_stride, static_cast<uint16_t*>(p.k_pool) + sh.at[i], p.stride_head, hq, hk,
+           true);
+      rows(p.v + t * p.v_stride, static_cast<uint16_t*>(p.v_pool) + sh.at[i], p.stride_head, hq + hk,
+           hk, false);
     }
   }
 }
@@ -410,13 +425,11 @@ __device__ __forceinline__ bool find_block(const AppendParams& p, int item, Bloc
 }
 
 template <int BS, int CACHE>
-__device__ __forceinline__ void block_role(const AppendParams& p, int item, int h,
-                                           BlockShared<BS>& sh) {
+__device__ __forceinline__ void block_role(const AppendParams& p, int h, BlockShared<BS>& sh) {
   constexpr bool kBf16 = CACHE == SEER_CACHE_BF16;
   constexpr int kThreads = BS * 4;                      // two rows per group of 8 threads
   constexpr int kGroups = kThreads / kRowThreads;       // BS / 2
   constexpr int kBytes = kBf16 ? 2 : 1;                 // per cached element
-  if (!find_block<BS>(p, item, sh)) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = tid / kRowThreads, i = tid % kRowThreads;
   const Seq s = sh.seq;
@@ -476,7 +489,7 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int item, int 
       widen8(keys[r * 16 + sl.c0], x[u]);
       widen8(keys[r * 16 + sl.c1], x[u] + 8);
       if (sl.turned0 || sl.turned1)
-        turn16(p, sl, rope_row(p, s.first + (base + r - past), base + r), x[u]);
+        turn16(p, sl, load_turn(p, sl, rope_row(p, s.first + (base + r - past), base + r)), x[u]);
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[u][e] = 0.f;
@@ -627,10 +640,19 @@ __global__ void __launch_bounds__(BS * 4, BS == 64 ? 4 : 2) append_blocks_kernel
   extern __shared__ __align__(16) uint8_t ap_raw[];
   pdl_wait();
   pdl_launch_dependents();
-  const int n_blk = p.items * p.Hkv;
+  const int n_blk = p.items * (p.Hkv / p.heads);
   const int c = (int)blockIdx.x;
-  if (c < n_blk) block_role<BS, CACHE>(p, c / p.Hkv, c % p.Hkv, *reinterpret_cast<BlockShared<BS>*>(ap_raw));
-  else row_role(p, c - n_blk, *reinterpret_cast<RowShared*>(ap_raw));
+  if (c < n_blk) {
+    BlockShared<BS>& sh = *reinterpret_cast<BlockShared<BS>*>(ap_raw);
+    const int per_block = p.Hkv / p.heads;  // CTAs of one block
+    if (!find_block<BS>(p, c / per_block, sh)) return;
+    for (int i = 0; i < p.heads; ++i) {
+      if (i > 0) __syncthreads();  // the pooled key is read out of shared memory
+      block_role<BS, CACHE>(p, (c % per_block) * p.heads + i, sh);
+    }
+  } else {
+    row_role(p, c - n_blk, *reinterpret_cast<RowShared*>(ap_raw));
+  }
 }
 
 __global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p) {
@@ -668,13 +690,22 @@ static cudaError_t launch_blocks(const AppendParams& p, int64_t grid, cudaStream
                        stream);
 }
 
-cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream) {
+cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
   p.rows_kv = cache == SEER_CACHE_BF16 && p.kbar == nullptr;
   const int R = (p.q != nullptr ? p.Hq : 0) + (p.rows_kv ? 2 * p.Hkv : 0);
   int64_t tiles = 0;
   if (R > 0) {
-    p.tile_tokens = kRowTileRows / R;
+    // a warp's share of a token: all its rows, or a part of them where there
+    // are too few tokens to keep the SMs busy; a CTA's tile: some kRowTileRows
+    // rows (its start -- sequences, lengths, pages, three dependent loads -- costs
+    // as much as some 100 rows: 2 x 16K prompt with 56 rows a token, tiles of
+    // 128 / 384 / 1024 rows 194 / 177 / 187 us)
+    int64_t seg = (32 * (int64_t)num_sms + p.T - 1) / p.T;
+    if (seg > (R + 3) / 4) seg = (R + 3) / 4;
+    p.segment_rows = (int)(((R + seg - 1) / seg + 3) / 4 * 4);
+    p.segments = (R + p.segment_rows - 1) / p.segment_rows;
+    p.tile_tokens = p.segments > 1 ? 8 / p.segments : kRowTileRows / R;
     if (p.tile_tokens < 1) p.tile_tokens = 1;
     if (p.tile_tokens > kMaxTileTokens) p.tile_tokens = kMaxTileTokens;
     tiles = ((int64_t)p.T + p.tile_tokens - 1) / p.tile_tokens;
@@ -687,7 +718,12 @@ cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream) {
   const int64_t by_rows = (int64_t)p.T / p.bs + 2 * (int64_t)p.B;
   if (p.max_new > 1 && by_rows < items) items = by_rows;
   p.items = (int)items;
-  const int64_t grid = items * p.Hkv + tiles;
+  // heads of a block per CTA: as many as leave the SMs' resident CTAs twice
+  // over (finding the block and its page are paid once for them)
+  p.heads = 1;
+  for (int hc = 2; hc <= p.Hkv && items * (p.Hkv / hc) >= 8 * (int64_t)num_sms; ++hc)
+    if (p.Hkv % hc == 0) p.heads = hc;
+  const int64_t grid = items * (p.Hkv / p.heads) + tiles;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (p.bs == 64) {
     if (cache == SEER_CACHE_BF16) return launch_blocks<64, SEER_CACHE_BF16>(p, grid, stream);

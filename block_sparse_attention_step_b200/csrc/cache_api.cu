@@ -266,7 +266,7 @@ seer_status seer_append_rope(const seer_dims* d, const seer_append_args* a, seer
   p.stride_page = d->stride_page;
   p.stride_token = d->stride_token;
   p.stride_head = d->stride_head;
-  SEER_CUDA(run_append_rope(p, a->cache_type, stream));
+  SEER_CUDA(run_append_rope(p, a->cache_type, num_sms_current(), stream));
   return SEER_OK;
 }
 

@@ -29,10 +29,12 @@ struct AppendParams {
   // set by the launcher
   int rows_kv;      // the row role writes k and v too (bf16, no pooled keys)
   int tile_tokens;  // tokens of a row-role tile
+  int segments, segment_rows;  // parts a token's rows are cut into, one warp each
   int items;        // touched blocks at most
+  int heads;        // KV heads of a block per CTA (divides Hkv)
 };
 
-cudaError_t run_append_rope(AppendParams p, int cache, cudaStream_t stream);
+cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t stream);
 cudaError_t run_rope_table(float* table, int max_position, int rot, double base,
                            cudaStream_t stream);
 
