@@ -37,6 +37,7 @@
 
 #include "block_mean.cuh"
 #include "cache_ops.cuh"
+#include "packed.cuh"
 #include "ragged.cuh"
 
 namespace seer {
@@ -214,10 +215,12 @@ __device__ __forceinline__ void turn16(const AppendParams& p, const Slot& s, con
   } else if (s.turned0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      turn(x[4 * k], x[8 + 4 * k], t.c[k].x, t.w[k].x);
-      turn(x[4 * k + 1], x[9 + 4 * k], t.c[k].y, t.w[k].y);
-      turn(x[4 * k + 2], x[10 + 4 * k], t.c[k].z, t.w[k].z);
-      turn(x[4 * k + 3], x[11 + 4 * k], t.c[k].w, t.w[k].w);
+      float* a = x + 4 * k;
+      float* b = x + 8 + 4 * k;
+      turn(a[0], b[0], t.c[k].x, t.w[k].x);
+      turn(a[1], b[1], t.c[k].y, t.w[k].y);
+      turn(a[2], b[2], t.c[k].z, t.w[k].z);
+      turn(a[3], b[3], t.c[k].w, t.w[k].w);
     }
   }
 }
@@ -351,10 +354,6 @@ struct BlockShared {
   __align__(16) uint8_t values[BS * kHeadDim * 2];
   __align__(16) float part[kPoolWarps * kHeadDim];
   float red[2][BS / 8];  // one per warp
-  int scan[BS / 8];
-  int b, j;
-  Seq seq;
-  float scale[2], shrink[2];
 };
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -367,201 +366,240 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
-// Item number -> (sequence, touched block); false: past the last one.
-template <int BS>
-__device__ __forceinline__ bool find_block(const AppendParams& p, int item, BlockShared<BS>& sh) {
-  constexpr int kThreads = BS * 4;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) sh.b = -1;
-  __syncthreads();
+// Item number -> (sequence, touched block) and that sequence's rows; b < 0: past
+// the last one.  Every warp works it out for itself, a sequence per lane.
+struct Touched {
+  int b, j;
+  Seq seq;
+};
+
+__device__ __forceinline__ Touched find_block(const AppendParams& p, int item) {
+  Touched t = {-1, 0, {0, 0, 0}};
   if (p.max_new == 1) {
-    if (tid == 0) {
-      const Seq s = load_seq(p, item);
+    const Seq s = load_seq(p, item);
+    if (s.n > 0) {
+      t.b = item;
+      t.j = (s.L - 1) / p.bs;
+      t.seq = s;
+    }
+    return t;
+  }
+  const int lane = threadIdx.x & 31;
+  int passed = 0;  // touched blocks of the sequences before this round
+  for (int base = 0; base < p.B && t.b < 0; base += 32) {
+    const int b = base + lane;
+    Seq s = {0, 0, 0};
+    int cnt = 0, j0 = 0;
+    if (b < p.B) {
+      s = load_seq(p, b);
       if (s.n > 0) {
-        sh.b = item;
-        sh.j = (s.L - 1) / p.bs;
-        sh.seq = s;
+        j0 = (s.L - s.n) / p.bs;
+        cnt = (s.L - 1) / p.bs - j0 + 1;
       }
     }
-  } else {
-    int passed = 0;  // touched blocks of the sequences before this chunk
-    for (int base = 0; base < p.B; base += kThreads) {
-      const int b = base + tid;
-      Seq s = {0, 0, 0};
-      int cnt = 0, j0 = 0;
-      if (b < p.B) {
-        s = load_seq(p, b);
-        if (s.n > 0) {
-          j0 = (s.L - s.n) / p.bs;
-          cnt = (s.L - 1) / p.bs - j0 + 1;
-        }
-      }
-      int incl = cnt;
+    int incl = cnt;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == 31) sh.scan[warp] = incl;
-      __syncthreads();
-      int off = passed, total = passed;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) off += sh.scan[w];
-        total += sh.scan[w];
-      }
-      const int lo = off + incl - cnt;
-      if (item >= lo && item < lo + cnt) {
-        sh.b = b;
-        sh.j = j0 + item - lo;
-        sh.seq = s;
-      }
-      passed = total;
-      __syncthreads();
-      if (passed > item) break;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
+    const int lo = passed + incl - cnt;
+    const unsigned hit = __ballot_sync(0xffffffffu, item >= lo && item < lo + cnt);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      t.b = base + src;
+      t.j = __shfl_sync(0xffffffffu, j0 + item - lo, src);
+      t.seq.first = __shfl_sync(0xffffffffu, s.first, src);
+      t.seq.n = __shfl_sync(0xffffffffu, s.n, src);
+      t.seq.L = __shfl_sync(0xffffffffu, s.L, src);
+    }
+    passed += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return t;
+}
+
+// The larger magnitude of two bf16 pairs, element by element; a NaN stays one.
+__device__ __forceinline__ uint32_t max2_abs(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return d;
+}
+
+// Both maxima over the CTA, in every thread (one barrier).
+template <int BS>
+__device__ __forceinline__ void block_max(float& ak, float& av, BlockShared<BS>& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ak = max_nan(ak, __shfl_xor_sync(0xffffffffu, ak, o));
+    av = max_nan(av, __shfl_xor_sync(0xffffffffu, av, o));
+  }
+  if (lane == 0) {
+    sh.red[0][warp] = ak;
+    sh.red[1][warp] = av;
   }
   __syncthreads();
-  return sh.b >= 0;
+  ak = sh.red[0][0];
+  av = sh.red[1][0];
+#pragma unroll
+  for (int w = 1; w < BS / 8; ++w) {
+    ak = max_nan(ak, sh.red[0][w]);
+    av = max_nan(av, sh.red[1][w]);
+  }
 }
 
 template <int BS, int CACHE>
-__device__ __forceinline__ void block_role(const AppendParams& p, int h, BlockShared<BS>& sh) {
+__device__ __forceinline__ void block_role(const AppendParams& p, const Touched& where, int h,
+                                           BlockShared<BS>& sh) {
   constexpr bool kBf16 = CACHE == SEER_CACHE_BF16;
   constexpr int kThreads = BS * 4;                      // two rows per group of 8 threads
   constexpr int kGroups = kThreads / kRowThreads;       // BS / 2
   constexpr int kBytes = kBf16 ? 2 : 1;                 // per cached element
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = tid / kRowThreads, i = tid % kRowThreads;
-  const Seq s = sh.seq;
-  const int b = sh.b, j = sh.j;
+  const Seq s = where.seq;
+  const int b = where.b, j = where.j;
   const int past = s.L - s.n;
   const int base = j * BS;                       // cache position of the block's row 0
   const int old_rows = max(0, past - base);      // rows it already holds
   const int end = min(BS, s.L - base);           // one past its last new row
-  const int64_t page = page_of(p.page_table, b, j, p.max_blocks);
-  if (page < 0 || page >= p.num_pages) {
-    if (tid == 0) flag_status(p.status, SEER_DEV_BAD_PAGE);
-    return;
-  }
   const Slot sl = slot_of(p, i);
-  const int64_t pool_at = page * p.stride_page + (int64_t)h * p.stride_head;
-  uint8_t* kp = static_cast<uint8_t*>(p.k_pool) + pool_at * kBytes;
-  uint8_t* vp = static_cast<uint8_t*>(p.v_pool) + pool_at * kBytes;
-  const int64_t row_bytes = p.stride_token * kBytes;
 
   // rows g and g + kGroups of the block, all reads in flight at once; a thread
   // fetches what it works on itself, so it waits for nobody else
-  uint4* keys = reinterpret_cast<uint4*>(sh.keys);
-  uint4* vals = reinterpret_cast<uint4*>(sh.values);
+  const int64_t t0 = s.first + (base + g - past);  // token of row g
+  const uint4* ks = reinterpret_cast<const uint4*>(p.k + t0 * p.k_stride + h * kHeadDim);
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v + t0 * p.v_stride + h * kHeadDim);
+  uint4* kh = reinterpret_cast<uint4*>(sh.keys) + g * 16;  // row g here; row g + kGroups: + kNext
+  uint4* vh = reinterpret_cast<uint4*>(sh.values) + g * 16;
+  constexpr int kNext = kGroups * 16;
   bool live[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = g + u * kGroups;
     live[u] = r >= old_rows && r < end;
     if (live[u]) {
-      const int64_t t = s.first + (base + r - past);
-      const uint4* ks = reinterpret_cast<const uint4*>(p.k + t * p.k_stride + (int64_t)h * kHeadDim);
-      const uint4* vs = reinterpret_cast<const uint4*>(p.v + t * p.v_stride + (int64_t)h * kHeadDim);
-      cp_async16(keys + r * 16 + sl.c0, ks + sl.c0);
-      cp_async16(keys + r * 16 + sl.c1, ks + sl.c1);
-      cp_async16(vals + r * 16 + sl.c0, vs + sl.c0);
-      cp_async16(vals + r * 16 + sl.c1, vs + sl.c1);
-    } else if (r < old_rows && p.kbar != nullptr) {
+      const uint4* k = u ? ks + kGroups / 8 * p.k_stride : ks;
+      const uint4* v = u ? vs + kGroups / 8 * p.v_stride : vs;
+      cp_async16(kh + u * kNext + sl.c0, k + sl.c0);
+      cp_async16(kh + u * kNext + sl.c1, k + sl.c1);
+      cp_async16(vh + u * kNext + sl.c0, v + sl.c0);
+      cp_async16(vh + u * kNext + sl.c1, v + sl.c1);
+    }
+  }
+  const int64_t page = page_of(p.page_table, b, j, p.max_blocks);
+  if (page < 0 || page >= p.num_pages) {  // the whole CTA
+    if (tid == 0) flag_status(p.status, SEER_DEV_BAD_PAGE);
+    cp_async_wait();
+    return;
+  }
+  const int64_t pool_at = page * p.stride_page + (int64_t)h * p.stride_head;
+  uint8_t* kp = static_cast<uint8_t*>(p.k_pool) + pool_at * kBytes;
+  uint8_t* vp = static_cast<uint8_t*>(p.v_pool) + pool_at * kBytes;
+  const int64_t row_bytes = p.stride_token * kBytes;
+  float old_k = 0.f, old_v = 0.f;  // the block's scales so far
+  if (old_rows > 0) {
+    if constexpr (!kBf16) {
+      old_k = p.k_scale[page * p.Hkv + h];
+      old_v = p.v_scale[page * p.Hkv + h];
+    }
+    if (p.kbar != nullptr) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int chunk = c ? sl.c1 : sl.c0;
-        if constexpr (kBf16) cp_async16(keys + r * 16 + chunk, kp + r * row_bytes + 16 * chunk);
-        else cp_async8(keys + r * 16 + chunk, kp + r * row_bytes + 8 * chunk);
+      for (int u = 0; u < 2; ++u) {
+        const int r = g + u * kGroups;
+        if (r >= old_rows) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int chunk = c ? sl.c1 : sl.c0;
+          if constexpr (kBf16) cp_async16(kh + u * kNext + chunk, kp + r * row_bytes + 16 * chunk);
+          else cp_async8(kh + u * kNext + chunk, kp + r * row_bytes + 8 * chunk);
+        }
       }
     }
   }
-  float old_scale = 0.f;
-  if constexpr (!kBf16) {
-    if (tid < 2 && old_rows > 0) old_scale = (tid == 0 ? p.k_scale : p.v_scale)[page * p.Hkv + h];
-  }
   cp_async_wait();
 
+  float key_scale = 1.f;
   float x[2][16];  // the new keys, turned
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int r = g + u * kGroups;
     if (live[u]) {
-      widen8(keys[r * 16 + sl.c0], x[u]);
-      widen8(keys[r * 16 + sl.c1], x[u] + 8);
+      widen8(kh[u * kNext + sl.c0], x[u]);
+      widen8(kh[u * kNext + sl.c1], x[u] + 8);
       if (sl.turned0 || sl.turned1)
-        turn16(p, sl, load_turn(p, sl, rope_row(p, s.first + (base + r - past), base + r)), x[u]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[u][e] = 0.f;
+        turn16(p, sl, load_turn(p, sl, rope_row(p, (int)t0 + u * kGroups, base + g + u * kGroups)),
+               x[u]);
     }
   }
+  uint8_t* kd = kp + g * row_bytes;  // row g of the page
+  uint8_t* vd = vp + g * row_bytes;
 
   if constexpr (kBf16) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int r = g + u * kGroups;
       if (!live[u]) continue;
       const uint4 a = round8(x[u]), c = round8(x[u] + 8);
-      uint4* kd = reinterpret_cast<uint4*>(kp + r * row_bytes);
-      uint4* vd = reinterpret_cast<uint4*>(vp + r * row_bytes);
-      kd[sl.c0] = a;
-      kd[sl.c1] = c;
-      vd[sl.c0] = vals[r * 16 + sl.c0];
-      vd[sl.c1] = vals[r * 16 + sl.c1];
-      keys[r * 16 + sl.c0] = a;
-      keys[r * 16 + sl.c1] = c;
+      uint4* ku = reinterpret_cast<uint4*>(kd + u * kGroups * row_bytes);
+      uint4* vu = reinterpret_cast<uint4*>(vd + u * kGroups * row_bytes);
+      ku[sl.c0] = a;
+      ku[sl.c1] = c;
+      vu[sl.c0] = vh[u * kNext + sl.c0];
+      vu[sl.c1] = vh[u * kNext + sl.c1];
+      kh[u * kNext + sl.c0] = a;
+      kh[u * kNext + sl.c1] = c;
     }
   } else {
-    // largest finite magnitudes of the new rows
+    // largest magnitudes of the new rows (a NaN stays one)
     float ak = 0.f, av = 0.f;
-    bool fine = true;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (!live[u]) continue;
-      const int r = g + u * kGroups;
-      float y[16];
-      widen8(vals[r * 16 + sl.c0], y);
-      widen8(vals[r * 16 + sl.c1], y + 8);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float a = fabsf(x[u][e]), c = fabsf(y[e]);
-        if (a < INFINITY) ak = fmaxf(ak, a);
-        else fine = false;
-        if (c < INFINITY) av = fmaxf(av, c);
-        else fine = false;
+      for (int e = 0; e < 16; ++e) ak = max_nan(ak, fabsf(x[u][e]));
+      const uint4 a = vh[u * kNext + sl.c0], c = vh[u * kNext + sl.c1];
+      const uint32_t top = max2_abs(max2_abs(max2_abs(a.x, a.y), max2_abs(a.z, a.w)),
+                                    max2_abs(max2_abs(c.x, c.y), max2_abs(c.z, c.w)));
+      av = max_nan(av, max_nan(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u)));
+    }
+    block_max<BS>(ak, av, sh);
+    if (!(ak < INFINITY) || !(av < INFINITY)) {
+      // (the whole CTA) some value is not finite: over the finite ones
+      if (tid == 0) flag_status(p.status, SEER_DEV_NONFINITE_KV);
+      ak = av = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!live[u]) continue;
+        float y[16];
+        widen8(vh[u * kNext + sl.c0], y);
+        widen8(vh[u * kNext + sl.c1], y + 8);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (fabsf(x[u][e]) < INFINITY) ak = fmaxf(ak, fabsf(x[u][e]));
+          if (fabsf(y[e]) < INFINITY) av = fmaxf(av, fabsf(y[e]));
+        }
       }
+      __syncthreads();  // everyone has read the first maxima
+      block_max<BS>(ak, av, sh);
     }
-    if (!fine) flag_status(p.status, SEER_DEV_NONFINITE_KV);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
-      av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
+    // every thread works out both scales (the old ones were read by all before
+    // the barrier in block_max)
+    float shrink_k, shrink_v;
+    const float scale_k = grown_scale<CACHE>(old_k, ak, old_rows > 0, &shrink_k);
+    const float scale_v = grown_scale<CACHE>(old_v, av, old_rows > 0, &shrink_v);
+    if (tid == 0) {
+      if (old_rows == 0 || scale_k != old_k) p.k_scale[page * p.Hkv + h] = scale_k;
+      if (old_rows == 0 || scale_v != old_v) p.v_scale[page * p.Hkv + h] = scale_v;
     }
-    if (lane == 0) {
-      sh.red[0][warp] = ak;
-      sh.red[1][warp] = av;
-    }
-    __syncthreads();
-    if (tid < 2) {  // thread 0: k, thread 1: v
-      float a = 0.f;
-      for (int w = 0; w < kThreads / 32; ++w) a = fmaxf(a, sh.red[tid][w]);
-      float shrink;
-      const float now = grown_scale<CACHE>(old_scale, a, old_rows > 0, &shrink);
-      if (old_rows == 0 || now != old_scale)
-        (tid == 0 ? p.k_scale : p.v_scale)[page * p.Hkv + h] = now;
-      sh.scale[tid] = now;
-      sh.shrink[tid] = shrink;
-    }
-    __syncthreads();
-    const float inv_k = sh.scale[0] > 0.f ? __frcp_rn(sh.scale[0]) : 0.f;
-    const float inv_v = sh.scale[1] > 0.f ? __frcp_rn(sh.scale[1]) : 0.f;
-    const float shrink_k = sh.shrink[0], shrink_v = sh.shrink[1];
+    key_scale = scale_k;
+    const float inv_k = scale_k > 0.f ? __frcp_rn(scale_k) : 0.f;
+    const float inv_v = scale_v > 0.f ? __frcp_rn(scale_v) : 0.f;
     auto code8 = [](const float* y, float f) {
-      return make_uint2(
-          Code8<CACHE>::pack4(__fmul_rn(y[0], f), __fmul_rn(y[1], f), __fmul_rn(y[2], f),
-                              __fmul_rn(y[3], f)),
-          Code8<CACHE>::pack4(__fmul_rn(y[4], f), __fmul_rn(y[5], f), __fmul_rn(y[6], f),
-                              __fmul_rn(y[7], f)));
+      const uint64_t f2 = pack2(f, f);
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), f2), z[e], z[e + 1]);
+      return make_uint2(Code8<CACHE>::pack4(z[0], z[1], z[2], z[3]),
+                        Code8<CACHE>::pack4(z[4], z[5], z[6], z[7]));
     };
     auto recode = [&](uint2 w, float f) {
       float y[8];
@@ -571,28 +609,36 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int h, BlockSh
     };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int r = g + u * kGroups;
-      uint2* kd = reinterpret_cast<uint2*>(kp + r * row_bytes);
-      uint2* vd = reinterpret_cast<uint2*>(vp + r * row_bytes);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int chunk = c ? sl.c1 : sl.c0;
-        uint2* held = reinterpret_cast<uint2*>(keys + r * 16 + chunk);
-        if (live[u]) {
-          float y[8];
-          widen8(vals[r * 16 + chunk], y);
-          const uint2 ck = code8(x[u] + 8 * c, inv_k);
-          kd[chunk] = ck;
-          vd[chunk] = code8(y, inv_v);
-          *held = ck;
-        } else if (r < old_rows) {
-          // earlier rows: rounded again where the scale grew
-          if (shrink_k != 1.f) {
-            const uint2 w = recode(kd[chunk], shrink_k);
-            kd[chunk] = w;
-            *held = w;
-          }
-          if (shrink_v != 1.f) vd[chunk] = recode(vd[chunk], shrink_v);
+      uint2* ku = reinterpret_cast<uint2*>(kd + u * kGroups * row_bytes);
+      uint2* vu = reinterpret_cast<uint2*>(vd + u * kGroups * row_bytes);
+      uint2* h0 = reinterpret_cast<uint2*>(kh + u * kNext + sl.c0);
+      uint2* h1 = reinterpret_cast<uint2*>(kh + u * kNext + sl.c1);
+      if (live[u]) {
+        float y[16];
+        widen8(vh[u * kNext + sl.c0], y);
+        widen8(vh[u * kNext + sl.c1], y + 8);
+        const uint2 k0 = code8(x[u], inv_k), k1 = code8(x[u] + 8, inv_k);
+        const uint2 v0 = code8(y, inv_v), v1 = code8(y + 8, inv_v);
+        if (sl.c1 == sl.c0 + 1) {  // neighbouring chunks: 16 codes at once
+          *reinterpret_cast<uint4*>(ku + sl.c0) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+          *reinterpret_cast<uint4*>(vu + sl.c0) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        } else {
+          ku[sl.c0] = k0;
+          ku[sl.c1] = k1;
+          vu[sl.c0] = v0;
+          vu[sl.c1] = v1;
+        }
+        *h0 = k0;
+        *h1 = k1;
+      } else if (g + u * kGroups < old_rows) {
+        // earlier rows: rounded again where the scale grew
+        if (shrink_k != 1.f) {
+          *h0 = ku[sl.c0] = recode(ku[sl.c0], shrink_k);
+          *h1 = ku[sl.c1] = recode(ku[sl.c1], shrink_k);
+        }
+        if (shrink_v != 1.f) {
+          vu[sl.c0] = recode(vu[sl.c0], shrink_v);
+          vu[sl.c1] = recode(vu[sl.c1], shrink_v);
         }
       }
     }
@@ -613,17 +659,18 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int h, BlockSh
         a.w += __uint_as_float(w.y & 0xffff0000u);
       }
     } else {
-      const float scale = sh.scale[0];
+      // sums of at most 128 codes are exact (multiples of 2^-9 below 2^16), so
+      // the scale is applied once
       a = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int t = warp; t < end; t += kPoolWarps) {
         float y[4];
         // dims 4 lane .. 4 lane + 3: half of the codes in the first half of chunk lane / 2
         Code8<CACHE>::unpack4(
             reinterpret_cast<const uint32_t*>(sh.keys)[t * 64 + (lane >> 1) * 4 + (lane & 1)], y);
-        a.x = __fadd_rn(a.x, __fmul_rn(y[0], scale));
-        a.y = __fadd_rn(a.y, __fmul_rn(y[1], scale));
-        a.z = __fadd_rn(a.z, __fmul_rn(y[2], scale));
-        a.w = __fadd_rn(a.w, __fmul_rn(y[3], scale));
+        a.x += y[0];
+        a.y += y[1];
+        a.z += y[2];
+        a.w += y[3];
       }
     }
     *reinterpret_cast<float4*>(sh.part + warp * kHeadDim + 4 * lane) = a;
@@ -631,7 +678,7 @@ __device__ __forceinline__ void block_role(const AppendParams& p, int h, BlockSh
   __syncthreads();
   if (tid < kHeadDim)
     p.kbar[(((int64_t)b * p.Hkv + h) * p.max_blocks + j) * kHeadDim + tid] =
-        pool_finish(sh.part, tid, end);
+        pool_finish(sh.part, tid, end) * key_scale;
 }
 
 // --------------------------------------------------------------- launches
@@ -645,10 +692,11 @@ __global__ void __launch_bounds__(BS * 4, BS == 64 ? 4 : 2) append_blocks_kernel
   if (c < n_blk) {
     BlockShared<BS>& sh = *reinterpret_cast<BlockShared<BS>*>(ap_raw);
     const int per_block = p.Hkv / p.heads;  // CTAs of one block
-    if (!find_block<BS>(p, c / per_block, sh)) return;
+    const Touched where = find_block(p, c / per_block);
+    if (where.b < 0) return;
     for (int i = 0; i < p.heads; ++i) {
-      if (i > 0) __syncthreads();  // the pooled key is read out of shared memory
-      block_role<BS, CACHE>(p, (c % per_block) * p.heads + i, sh);
+      if (i > 0) __syncthreads();  // the head before is done with shared memory
+      block_role<BS, CACHE>(p, where, (c % per_block) * p.heads + i, sh);
     }
   } else {
     row_role(p, c - n_blk, *reinterpret_cast<RowShared*>(ap_raw));
