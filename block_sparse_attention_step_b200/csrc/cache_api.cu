@@ -74,14 +74,39 @@ seer_status make_rows_map(const uint16_t* q, const seer_dims* d, int T, int ntok
 
 constexpr int kClusterMax = 8;  // CTAs that join one row's pieces without a partial
 
-// Pieces per row: enough CTAs for every SM's resident slots, no piece below
-// two stages.
+// Pieces per row.  As many as fill the SMs' resident CTAs once, up to the 8 a
+// cluster joins (16 sequences x 8 heads, 52 stages of an e4m3 cache: 1 / 2 / 3 /
+// 4 / 8 pieces 30.0 / 27.3 / 27.3 / 35.5 / 39.0 us; a second wave costs each
+// piece's start again).  Past that, partials and a combine (2 us more) once a
+// piece of 8 would still run 10 stages (0.4 us each).  Rows that fill the SMs
+// several times over: no piece above 72 stages, which would run on alone at the
+// end (64 ragged sequences x 8 heads of up to 104 stages: 1 / 2 / 4 pieces 120.8 /
+// 111.7 / 116.1 us; of 66 stages, bf16: 1 / 2 pieces 146 / 156 us).
 int32_t pick_splits(const seer_dims* d, int64_t stages, int ctas_per_sm) {
   const int64_t rows = (int64_t)d->batch * d->num_kv_heads;
-  const int64_t slots = (int64_t)num_sms_current() * ctas_per_sm;
-  int32_t s = 1;
-  while (s < kMaxSplits && rows * s * 2 <= slots && stages >= 4 * s) s *= 2;
-  return s;
+  const int64_t fill = (int64_t)num_sms_current() * ctas_per_sm / rows;
+  int64_t s = fill < stages ? fill : stages;
+  if (s > kClusterMax) s = kClusterMax;
+  if (s < 1) s = 1;
+  if (stages >= 10 * kClusterMax) {
+    int64_t clusters = stages / (8 * kClusterMax);
+    if (clusters > fill / kClusterMax) clusters = fill / kClusterMax;
+    if (clusters > kMaxSplits / kClusterMax) clusters = kMaxSplits / kClusterMax;
+    if (clusters >= 2) s = clusters * kClusterMax;
+  }
+  if (stages > 72 * s) {
+    s = (stages + 71) / 72;
+    if (s > kClusterMax) s = kClusterMax;
+  }
+  return (int32_t)s;
+}
+
+// Stages of 64 tokens that the longest row of a window with sinks can have.
+int64_t window_stages(const seer_dims* d, int32_t window, int32_t sinks) {
+  int64_t blocks = ((int64_t)sinks + d->block_size - 1) / d->block_size +
+                   ((int64_t)window + d->block_size - 2) / d->block_size + 1;
+  if (blocks > d->max_blocks) blocks = d->max_blocks;
+  return blocks * (d->block_size / kTileTokens);
 }
 
 size_t split_bytes(const seer_dims* d, int32_t splits) {
@@ -104,7 +129,7 @@ seer_status cache_decode(const seer_dims* d, const seer_cache_attn_args* a, bool
       return SEER_ERR_INVALID_ARG;
   }
   const int32_t S = a->num_splits;
-  if (S < 1 || S > kMaxSplits || (S & (S - 1))) return SEER_ERR_INVALID_ARG;
+  if (S < 1 || S > kMaxSplits || (S > kClusterMax && S % kClusterMax)) return SEER_ERR_INVALID_ARG;
   if (!aligned(a->q, 16) || !aligned(a->out, 2)) return SEER_ERR_UNSUPPORTED;
   if ((int64_t)d->batch * d->num_kv_heads * S > INT_MAX) return SEER_ERR_UNSUPPORTED;
   const size_t need = split_bytes(d, S);
@@ -174,10 +199,7 @@ int32_t seer_sparse_decode_q8_splits(const seer_dims* d, int32_t k_max) {
 
 int32_t seer_window_decode_splits(const seer_dims* d, int32_t window, int32_t sinks) {
   if (check_dims(d) != SEER_OK || window < 1 || sinks < 0) return 1;
-  int64_t blocks = ((int64_t)sinks + d->block_size - 1) / d->block_size +
-                   ((int64_t)window + d->block_size - 2) / d->block_size + 1;
-  if (blocks > d->max_blocks) blocks = d->max_blocks;
-  return pick_splits(d, blocks * (d->block_size / kTileTokens), 2);
+  return pick_splits(d, window_stages(d, window, sinks), 2);
 }
 
 size_t seer_split_workspace_bytes(const seer_dims* d, int32_t num_splits) {

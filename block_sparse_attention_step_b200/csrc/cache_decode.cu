@@ -42,6 +42,7 @@
 #include <type_traits>
 
 #include "cache_ops.cuh"
+#include "ragged.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -179,16 +180,18 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full_bar[i], 1);
+      mbar_init(&full_bar[i], 2);  // the copies' arrival and the stage's record
       mbar_init(&empty_bar[i], kCDMath);
     }
     fence_mbar_init();
   }
+  __syncthreads();
+  pdl_wait();
   pdl_launch_dependents();
   const CDRow rw = cd_row<WINDOW>(p, row, b);
   const int lo = (int)((long long)s * rw.nst / S);
   const int n = (int)((long long)(s + 1) * rw.nst / S) - lo;
-  __syncthreads();
+  const int C = p.C;
 
   float m[NT][2], l[NT][2], o[8][NT][4];
 #pragma unroll
@@ -203,78 +206,109 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
     // ================================================================ copies
     const uint64_t policy = policy_evict_first();
     const int nsub = p.bs / kTileTokens;
+    // Stage t of the piece, one per lane: its block, then its page, then its
+    // scales, each a load that depends on the one before.  The next 32 stages
+    // go through them while the current 32 are issued.
+    auto block_of = [&](int t) {
+      const int e = (lo + t) / nsub;
+      if constexpr (WINDOW) return e < rw.sink_blocks ? e : rw.window_block + (e - rw.sink_blocks);
+      else return __ldg(p.idx + (int64_t)row * p.k_max + e);
+    };
+    const int nb = ceil_div_i(rw.L, p.bs);
+    auto page_at = [&](int t, int j) {  // -1: no such block; bad pages are flagged, page 0 is used
+      if (t >= n) return 0;
+      if (j < 0 || j >= nb) {
+        flag_status(p.status, SEER_DEV_BAD_INDEX);
+        return -1;
+      }
+      const int64_t pg = page_of(p.page_table, b, j, p.max_blocks);
+      if (pg >= 0 && pg < p.num_pages) return (int)pg;
+      flag_status(p.status, SEER_DEV_BAD_PAGE);
+      return 0;
+    };
+    auto scale_at = [&](const float* scale, int page) {
+      return kBf16 || page < 0 ? 1.f : __ldg(scale + (int64_t)page * p.Hkv + h);
+    };
     bool ok = true;
+    int j = lane < n ? block_of(lane) : 0;
+    int page = page_at(lane, j);
+    int next_j = 0, next_page = 0;
+    float ks = 1.f, vs = 1.f, next_ks = 1.f, next_vs = 1.f;
     for (int base = 0; base < n && ok; base += 32) {
-      // one stage per lane: its block, page and scales
-      const int t = base + lane;
-      int page = 0, tok = 0, sub = 0;
-      float ks = 1.f, vs = 1.f;
-      if (t < n) {
-        const int e = (lo + t) / nsub;
-        sub = (lo + t) - e * nsub;
-        int j;
-        if constexpr (WINDOW) j = e < rw.sink_blocks ? e : rw.window_block + (e - rw.sink_blocks);
-        else j = __ldg(p.idx + (int64_t)row * p.k_max + e);
-        if (j < 0 || j >= ceil_div_i(rw.L, p.bs)) {
-          flag_status(p.status, SEER_DEV_BAD_INDEX);
-          tok = 1 << 28;  // nothing of this stage is visible
-        } else {
-          tok = j * p.bs + sub * kTileTokens;
-          const int64_t pg = page_of(p.page_table, b, j, p.max_blocks);
-          if (pg < 0 || pg >= p.num_pages) flag_status(p.status, SEER_DEV_BAD_PAGE);
-          else page = (int)pg;  // else page 0: the copy stays inside the pool, the result is flagged
-          if constexpr (!kBf16) {
-            ks = __ldg(p.k_scale + (int64_t)page * p.Hkv + h);
-            vs = __ldg(p.v_scale + (int64_t)page * p.Hkv + h);
-          }
-        }
-      }
-      float lv = 0.f, inv = 1.f;
-      if constexpr (!kBf16) {
-        lv = vs == 0.f ? kZeroScaleLog2 : log2f(vs);
-        inv = vs == 0.f ? kZeroScaleInv : 1.f / vs;
-        if (vs == 0.f) sub |= 256;  // carried in the meta's sign of ks (scales are >= 0)
-      }
       const int cnt = min(32, n - base);
-      for (int i = 0; i < cnt; ++i) {
-        const int g_page = __shfl_sync(0xffffffffu, page, i);
-        const int g_tok = __shfl_sync(0xffffffffu, tok, i);
-        const int g_sub = __shfl_sync(0xffffffffu, sub, i);
-        const float g_ks = __shfl_sync(0xffffffffu, ks, i);
-        const float g_lv = __shfl_sync(0xffffffffu, lv, i);
-        const float g_inv = __shfl_sync(0xffffffffu, inv, i);
+      const int tok = page < 0 ? 1 << 28  // nothing of this stage is visible
+                               : j * p.bs + (lo + base + lane) % nsub * kTileTokens;
+      auto issue = [&](int i) {  // stage i of this round
         const int k = base + i, slot = k % kStages;
-        if (lane == 0 && !mbar_wait(&empty_bar[slot], ((k / kStages) & 1) ^ 1)) {
-          flag_status(p.status, SEER_DEV_TIMEOUT);
-          ok = false;
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (lane == 0) {
-          CDMeta mt;
-          mt.base = g_tok;
-          mt.ks = g_ks;
-          mt.lv = g_lv;
-          mt.inv = (g_sub & 256) ? -g_inv : g_inv;  // negative: the codes count as zero
-          meta[slot] = mt;
+        const int pg = max(0, __shfl_sync(0xffffffffu, page, i));
+        const int sub = (lo + k) % nsub;
+        if (elect_one()) {
           uint8_t* kd = ring + slot * Shape::kStageBytes;
           uint8_t* vd = kd + Shape::kTileBytes;
-          const int t0 = (g_sub & 255) * kTileTokens;
+          const int t0 = sub * kTileTokens;
           const int c1 = p.token_inner ? t0 : h, c2 = p.token_inner ? h : t0;
           mbar_arrive_expect_tx(&full_bar[slot], Shape::kStageBytes);
           if constexpr (kBf16) {
             constexpr int kHalf = Shape::kTileBytes / 2;
-            tma_load_4d(kd, &tm_k, 0, c1, c2, g_page, &full_bar[slot], policy);
-            tma_load_4d(kd + kHalf, &tm_k, 64, c1, c2, g_page, &full_bar[slot], policy);
-            tma_load_4d(vd, &tm_v, 0, c1, c2, g_page, &full_bar[slot], policy);
-            tma_load_4d(vd + kHalf, &tm_v, 64, c1, c2, g_page, &full_bar[slot], policy);
+            tma_load_4d(kd, &tm_k, 0, c1, c2, pg, &full_bar[slot], policy);
+            tma_load_4d(kd + kHalf, &tm_k, 64, c1, c2, pg, &full_bar[slot], policy);
+            tma_load_4d(vd, &tm_v, 0, c1, c2, pg, &full_bar[slot], policy);
+            tma_load_4d(vd + kHalf, &tm_v, 64, c1, c2, pg, &full_bar[slot], policy);
           } else {
-            tma_load_4d(kd, &tm_k, 0, c1, c2, g_page, &full_bar[slot], policy);
-            tma_load_4d(vd, &tm_v, 0, c1, c2, g_page, &full_bar[slot], policy);
+            tma_load_4d(kd, &tm_k, 0, c1, c2, pg, &full_bar[slot], policy);
+            tma_load_4d(vd, &tm_v, 0, c1, c2, pg, &full_bar[slot], policy);
           }
         }
         __syncwarp();
+      };
+      const int t_next = base + 32 + lane;
+      if (base + 32 < n) next_j = t_next < n ? block_of(t_next) : 0;
+      // the ring's first copies go out before the scales are here
+      int issued = 0;
+      if (base == 0) {
+        ks = scale_at(p.k_scale, page);
+        vs = scale_at(p.v_scale, page);
+        for (; issued < min(cnt, kStages); ++issued) issue(issued);
       }
+      float lv = 0.f, inv = 1.f;
+      if constexpr (!kBf16) {
+        // negative inverse: the scale is zero and the codes count as zero
+        lv = vs == 0.f ? kZeroScaleLog2 : log2f(vs);
+        inv = vs == 0.f ? -kZeroScaleInv : 1.f / vs;
+      }
+      for (int i = 0; i < cnt; ++i) {
+        const int k = base + i, slot = k % kStages;
+        if (i >= issued) {
+          ok = mbar_hold(&empty_bar[slot], ((k / kStages) & 1) ^ 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            flag_status(p.status, SEER_DEV_TIMEOUT);
+            break;
+          }
+          issue(i);
+        }
+        CDMeta mt;
+        mt.base = __shfl_sync(0xffffffffu, tok, i);
+        mt.ks = __shfl_sync(0xffffffffu, ks, i);
+        mt.lv = __shfl_sync(0xffffffffu, lv, i);
+        mt.inv = __shfl_sync(0xffffffffu, inv, i);
+        if (lane == 0) {
+          meta[slot] = mt;
+          mbar_arrive(&full_bar[slot]);
+        }
+        __syncwarp();
+        if (base + 32 < n) {
+          if (i == 8) next_page = page_at(t_next, next_j);
+          if (i == 16) {
+            next_ks = scale_at(p.k_scale, next_page);
+            next_vs = scale_at(p.v_scale, next_page);
+          }
+        }
+      }
+      j = next_j;
+      page = next_page;
+      ks = next_ks;
+      vs = next_vs;
     }
   } else {
     // ================================================================== math
@@ -328,7 +362,7 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
     bool ok = true;
     for (int k = 0; k < n; ++k) {
       const int slot = k % kStages;
-      ok = mbar_wait(&full_bar[slot], (k / kStages) & 1);
+      ok = mbar_hold(&full_bar[slot], (k / kStages) & 1);
       if (!__all_sync(0xffffffffu, ok)) {
         flag_status(p.status, SEER_DEV_TIMEOUT);
         break;
@@ -543,7 +577,7 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
   // case one of them gave up.
   if (warp == kCDMath && lane == 0) {
     for (int k = max(0, n - kStages); k < n; ++k)
-      if (!mbar_wait(&full_bar[k % kStages], (k / kStages) & 1))
+      if (!mbar_hold(&full_bar[k % kStages], (k / kStages) & 1))
         flag_status(p.status, SEER_DEV_TIMEOUT);
   }
   __syncthreads();
@@ -578,7 +612,6 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
     }
   }
   __syncthreads();
-  const int C = p.C;
   float* co = ow + (size_t)kCDMath * G * kHeadDim;  // the CTA's state [head][dim]
   for (int e = threadIdx.x; e < G * kHeadDim; e += kCDThreads) {
     const int g = e / kHeadDim;
@@ -599,7 +632,7 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
       cta_ml[1][g] = L;
     }
   }
-  // ---- join the cluster's CTAs: each takes every C-th part of the outputs
+  // ---- join the cluster's CTAs: each takes its part of the outputs
   cg::cluster_group cluster = cg::this_cluster();
   if (C > 1) cluster.sync();
   else __syncthreads();
@@ -651,13 +684,15 @@ static cudaError_t launch_cache_decode(const CUtensorMap& tk, const CUtensorMap&
   cfg.blockDim = dim3(kCDThreads);
   cfg.dynamicSmemBytes = CDShape<CACHE>::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)p.C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, tk, tv, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

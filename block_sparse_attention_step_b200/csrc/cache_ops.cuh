@@ -53,7 +53,7 @@ struct CacheDecodeParams {
   float* lse_out;  // optional
   int32_t* status;
   int B, Hq, Hkv, G, bs, max_blocks, k_max, window, sinks;
-  int S, C;         // pieces per row, CTAs per cluster (both powers of two, C <= 8 divides S)
+  int S, C;         // pieces per row, CTAs per cluster (C = min(S, 8), divides S)
   int token_inner;  // tensor map dims are (D, token, head, page), not (D, head, token, page)
   int64_t num_pages;
   float scale_log2;

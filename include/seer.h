@@ -561,7 +561,7 @@ SEER_API seer_status seer_append_rope(const seer_dims *d, const seer_append_args
  * does not see weigh nothing, whatever the cache holds there.  A row that
  * sees no token (seqlens[b] or n_sel 0) gets out 0 and lse -inf.
  *
- * num_splits (a power of two up to 64) pieces of a row run side by side.  Up
+ * num_splits (1 to 8, or 16, 24, .. 64) pieces of a row run side by side.  Up
  * to 8 are joined inside one thread-block cluster; more need a workspace of
  * seer_split_workspace_bytes() bytes (256-byte aligned, no initial contents;
  * calls that share one must not overlap).  The *_splits helpers pick a number

@@ -182,7 +182,7 @@ def draw_lists(c, seed, share):
 @pytest.mark.gpu
 @pytest.mark.parametrize("cache", ["e4m3", "int8"])
 @pytest.mark.parametrize("G", [1, 3, 5, 8, 12, 16])
-@pytest.mark.parametrize("bs,layout,splits", [(64, "nhd", 1), (128, "hnd", 4), (64, "hnd", 16)])
+@pytest.mark.parametrize("bs,layout,splits", [(64, "nhd", 1), (128, "hnd", 3), (64, "hnd", 16), (128, "nhd", 7)])
 def test_sparse_decode_q8(cache, G, bs, layout, splits):
     require_gpu()
     c = make_cache([0, 1, 63, 65, 1000], 2, bs, cache, layout, seed=G)
@@ -278,7 +278,7 @@ def test_window_decode_groups(cache, G):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("splits", [8, 16, 64])
+@pytest.mark.parametrize("splits", [6, 8, 24, 64])
 def test_long_row_is_split_and_deterministic(splits):
     """One row of 20,000 tokens; the same bits from every call."""
     require_gpu()
