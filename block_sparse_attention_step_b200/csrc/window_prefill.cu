@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kWPThreads, 2)
 
   // ---- which sequence and which of its token tiles (warp 0); meanwhile
   // tensor memory (warp 1), barriers (warp 2), tensor maps (warp 3)
+  pdl_launch_dependents();
   if (warp == 0) {
+    pdl_wait();  // every other read of global memory comes after the barrier below
     int passed = 0, found_b = -1, found_tile = 0;
     Seq found = {0, 0, 0};
     for (int base = 0; base < p.B && found_b < 0; base += 32) {
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       prefetch_tensormap(&tm_q);
       prefetch_tensormap(&tm_k);
       prefetch_tensormap(&tm_v);
+      pdl_wait();
       // after a wait has run out somewhere in the grid, later CTAs do no work
       // (each run-out wait costs about a second); one thread decides for all
       bars.stop = p.status != nullptr &&
@@ -524,7 +527,18 @@ cudaError_t run_window_prefill(const CUtensorMap& tq, const CUtensorMap& tk, con
   const int64_t by_rows = p.T / p.ntok + p.B;
   if (by_rows < tiles) tiles = by_rows;
   if (tiles * p.Hkv > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  window_prefill_kernel<<<(unsigned)(tiles * p.Hkv), kWPThreads, kWPSmem, stream>>>(tq, tk, tv, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.Hkv));
+  cfg.blockDim = dim3(kWPThreads);
+  cfg.dynamicSmemBytes = kWPSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, window_prefill_kernel, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

@@ -493,10 +493,11 @@ def _keep(a, *tensors):
 
 def _call(fn: str, d, a, stream):
     """A cache operator on its tensors' device, which has to be the current one."""
-    if a.device != torch.cuda.current_device():
-        raise ValueError(f"{fn}: tensors on cuda:{a.device}, current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    status = getattr(_lib(), fn)(ctypes.byref(d), ctypes.byref(a), _stream(stream))
+    device = torch.cuda.current_device()
+    if a.device != device:
+        raise ValueError(f"{fn}: tensors on cuda:{a.device}, current device is cuda:{device}")
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    status = getattr(_lib_handle or _lib(), fn)(ctypes.byref(d), ctypes.byref(a), raw)
     if status != SEER_OK:
         raise SeerError(fn, status)
 

@@ -1,0 +1,201 @@
+"""The paged-cache operators in a row, as a server runs them: an 8-bit cache
+with the gate, the selection and the decode; the rotary append feeding the
+bf16 step; two streams with caches of their own."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_attention_step_b200 import seer
+from oracle import cache_oracle as C
+from oracle import seer_oracle as O
+
+from gpu_util import MARGIN, require_gpu
+
+D = 128
+SCALE = 1 / math.sqrt(D)
+
+
+def rows(T, Hq, Hkv, g):
+    x = torch.randn((T, (Hq + 2 * Hkv) * D), generator=g).bfloat16().cuda()
+    return [y.unflatten(1, (-1, D)) for y in x.split([Hq * D, Hkv * D, Hkv * D], 1)]
+
+
+class Server:
+    """A ragged batch over one paged cache."""
+
+    def __init__(self, cache, B=3, Hq=8, Hkv=2, bs=64, blocks=16, seed=0):
+        self.B, self.Hq, self.Hkv, self.bs, self.cache = B, Hq, Hkv, bs, cache
+        self.g = torch.Generator().manual_seed(seed)
+        pages = B * blocks + 3
+        dtype = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}[cache]
+        self.kp, self.vp = [torch.zeros((pages, bs, Hkv, D), device="cuda").to(dtype) for _ in range(2)]
+        self.ks = self.vs = None
+        if cache != "bf16":
+            self.ks, self.vs = [torch.full((pages, Hkv), float("nan"), device="cuda") for _ in range(2)]   # first rows set them
+        self.table = torch.randperm(pages, generator=self.g)[:B * blocks].view(B, blocks).int().cuda()
+        self.d = seer.make_dims(B, Hq, Hkv, D, bs, blocks, pages)
+        self.kbar = torch.zeros((B, Hkv, blocks, D), device="cuda")
+        self.rope = seer.seer_rope_table(blocks * bs, 128)
+        self.w_gate = (torch.randn((Hkv, D, D), generator=self.g) / math.sqrt(D)).cuda()
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.lens, self.blocks = [0] * B, blocks
+
+    def append(self, new):
+        q, k, v = rows(sum(new), self.Hq, self.Hkv, self.g)
+        self.lens = [x + n for x, n in zip(self.lens, new)]
+        self.seqlens = torch.tensor(self.lens, dtype=torch.int32).cuda()
+        cu = torch.tensor([sum(new[:i]) for i in range(self.B + 1)], dtype=torch.int32).cuda()
+        self.q = torch.empty((sum(new), self.Hq, D), dtype=torch.bfloat16, device="cuda")
+        seer.seer_append_rope(self.d, seer.append_args(k, v, self.kp, self.vp, self.table, self.seqlens, q=q, q_out=self.q, rope=self.rope, cu_tokens=cu,
+                                                       max_new=max(new), k_scale=self.ks, v_scale=self.vs, kbar=self.kbar, dev_status=self.status))
+
+    def held(self, b, h):
+        """(K, V) [L][D] in fp64 as the cache holds them."""
+        L = self.lens[b]
+        t = np.arange(L)
+        pages = self.table[b].cpu().numpy()[t // self.bs]
+        out = []
+        for pool, scale in ((self.kp, self.ks), (self.vp, self.vs)):
+            if self.cache == "bf16":
+                x = pool[:, :, h].double().cpu().numpy()
+            else:
+                x = pool[:, :, h].contiguous()
+                x = C.e4m3_value(x.view(torch.uint8).cpu().numpy()) if self.cache == "e4m3" else x.double().cpu().numpy()
+                x = x * scale[:, h].double().cpu().numpy()[:, None, None]
+            out.append(x[pages, t % self.bs])
+        return out
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+def test_append_gate_select_and_decode_over_an_8_bit_cache(cache):
+    require_gpu()
+    s = Server(cache)
+    s.append([400, 130, 64])
+    k_max = 3
+    k_per_seq = torch.full((s.B,), k_max, dtype=torch.int32, device="cuda")
+    for step in range(3):
+        s.append([1, 1, 1])
+        scores = torch.empty((s.B, s.Hkv, s.blocks), device="cuda")
+        idx = torch.empty((s.B, s.Hkv, k_max), dtype=torch.int32, device="cuda")
+        n_sel = torch.empty((s.B, s.Hkv), dtype=torch.int32, device="cuda")
+        out, lse = torch.empty((s.B, s.Hq, D), dtype=torch.bfloat16, device="cuda"), torch.empty((s.B, s.Hq), device="cuda")
+        seer.seer_gate_scores(s.d, s.q, s.w_gate, s.kbar, s.seqlens, SCALE, scores, s.status)
+        seer.seer_block_select(s.d, scores, s.seqlens, k_per_seq, True, k_max, idx, n_sel, s.status)
+        splits = seer.seer_sparse_decode_q8_splits(s.d, k_max)
+        a = seer.sparse_decode_q8_args(s.q, s.kp, s.vp, s.table, s.seqlens, idx, n_sel, k_scale=s.ks, v_scale=s.vs, k_max=k_max, num_splits=splits,
+                                       softmax_scale=SCALE, out=out, lse_out=lse, dev_status=s.status)
+        seer.seer_sparse_decode_q8(s.d, a)
+        torch.cuda.synchronize()
+        assert s.status.item() == 0
+        got = out.double().cpu().numpy()
+        for b in range(s.B):
+            L = s.lens[b]
+            for h in range(s.Hkv):
+                K, V = s.held(b, h)
+                G = s.Hq // s.Hkv
+                q = s.q[b, h * G:(h + 1) * G].double().cpu().numpy()
+                nb = -(-L // s.bs)
+                kbar = np.stack([K[j * s.bs:(j + 1) * s.bs].mean(0) for j in range(nb)])
+                # pooled keys: fp32 sums of up to 64 held rows
+                assert np.abs(s.kbar[b, h, :nb].double().cpu().numpy() - kbar).max() <= 64 * 2.0 ** -24 * np.abs(K).max() + 2.0 ** -24 * np.abs(kbar).max()
+                want_scores = kbar @ (s.w_gate[h].double().cpu().numpy() @ q.mean(0)) * SCALE
+                merit = want_scores[:nb - 1]
+                order = np.sort(merit)[::-1]
+                chosen = idx[b, h, :int(n_sel[b, h])].cpu().tolist()
+                if len(order) <= k_max - 1 or order[k_max - 2] - order[k_max - 1] > MARGIN:
+                    assert chosen == sorted([nb - 1] + np.argsort(-merit, kind="stable")[:k_max - 1].tolist())
+                seen = np.isin(np.arange(L) // s.bs, chosen)
+                for i in range(G):
+                    want, want_lse = C.softmax_attention(q[i], K, V, seen, SCALE)
+                    # weights in f16 (2^-11), out in bf16 (2^-8)
+                    w = np.exp(K[seen] @ q[i] * SCALE - want_lse)
+                    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 1e-4) * (w @ np.abs(V[seen]) + np.abs(want))
+                    assert (np.abs(got[b, h * G + i] - want) <= tol).all()
+
+
+@pytest.mark.gpu
+def test_rotary_append_feeds_the_bf16_step():
+    """Pooled keys written by the append make the step's result the same bits as its own full pooling."""
+    require_gpu()
+    s = Server("bf16", seed=3)
+    s.append([400, 130, 64])
+    s.append([1, 1, 1])
+    k_max, splits = 3, 2
+    outs = []
+    for update, kbar in ((0, s.kbar), (2, torch.zeros_like(s.kbar))):
+        ws = torch.empty(seer.seer_step_workspace_bytes(s.d, k_max, splits), dtype=torch.uint8, device="cuda")
+        seer.seer_step_workspace_init(s.d, k_max, splits, ws)
+        out, lse = torch.empty((s.B, s.Hq, D), dtype=torch.bfloat16, device="cuda"), torch.empty((s.B, s.Hq), device="cuda")
+        a = seer.step_args(s.q, s.kp, s.vp, s.table, s.seqlens, s.w_gate, kbar, torch.full((s.B,), k_max, dtype=torch.int32, device="cuda"), update_kbar=update,
+                           force_newest=True, k_max=k_max, num_splits=splits, gate_scale=SCALE, softmax_scale=SCALE, workspace=ws, out=out, lse_out=lse,
+                           dev_status=s.status)
+        seer.seer_decode_step(s.d, a)
+        outs.append((out, lse))
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.gpu
+def test_calls_that_follow_each_other_at_once():
+    """Append and decode of one cache and prefill of another, 40 rounds enqueued without a wait: every call sees what
+    the one before it wrote (the launches overlap their starts)."""
+    require_gpu()
+    s = Server("e4m3", B=2, Hq=8, Hkv=2, seed=5, blocks=8)
+    s.append([64, 100])
+    base = s.lens
+    outs, steps = [], 40
+    out = [torch.empty((s.B, s.Hq, D), dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+    args, keep = [], []
+    for i in range(steps):
+        q, k, v = rows(2, s.Hq, s.Hkv, s.g)
+        lens = torch.tensor([x + i + 1 for x in base], dtype=torch.int32).cuda()
+        qr = torch.empty((2, s.Hq, D), dtype=torch.bfloat16, device="cuda")
+        args.append((seer.append_args(k, v, s.kp, s.vp, s.table, lens, q=q, q_out=qr, rope=s.rope, k_scale=s.ks, v_scale=s.vs, kbar=s.kbar, dev_status=s.status),
+                     seer.window_decode_args(qr, s.kp, s.vp, s.table, lens, window=90, sinks=4, num_splits=2, softmax_scale=SCALE, out=out[i], k_scale=s.ks,
+                                             v_scale=s.vs, dev_status=s.status)))
+        keep.append(qr)
+    pools = [x.clone() for x in (s.kp.view(torch.uint8), s.vp.view(torch.uint8), s.ks, s.vs)]
+    torch.cuda.synchronize()
+    for a, w in args:                                   # at once
+        seer.seer_append_rope(s.d, a)
+        seer.seer_window_decode(s.d, w)
+    torch.cuda.synchronize()
+    first = [x.clone() for x in out]
+    for x, y in zip((s.kp.view(torch.uint8), s.vp.view(torch.uint8), s.ks, s.vs), pools):
+        x.copy_(y)
+    for a, w in args:                                   # one by one
+        seer.seer_append_rope(s.d, a)
+        torch.cuda.synchronize()
+        seer.seer_window_decode(s.d, w)
+        torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(first, out)) and s.status.item() == 0
+
+
+@pytest.mark.gpu
+def test_two_streams_with_their_own_caches():
+    require_gpu()
+    servers = [Server("int8", seed=i) for i in (7, 8)]
+    for s in servers:
+        s.append([300, 70, 1])
+    torch.cuda.synchronize()
+    outs = []
+    for at_once in (True, False):
+        got = []
+        for s in servers:
+            out = torch.zeros((s.B, s.Hq, D), dtype=torch.bfloat16, device="cuda")
+            q = s.q[[s.lens[0] - 1, s.lens[0] + s.lens[1] - 1, sum(s.lens) - 1]].contiguous()
+            a = seer.window_decode_args(q, s.kp, s.vp, s.table, s.seqlens, window=250, sinks=2, num_splits=4, softmax_scale=SCALE, out=out, k_scale=s.ks, v_scale=s.vs)
+            got.append((s, a, out))
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()] if at_once else [None, None]
+        for _ in range(10):
+            for (s, a, out), st in zip(got, streams):
+                seer.seer_window_decode(s.d, a, st)
+        torch.cuda.synchronize()
+        outs.append([x[2] for x in got])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
