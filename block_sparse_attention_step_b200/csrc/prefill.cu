@@ -195,7 +195,7 @@ struct TcBars {
   uint64_t k_full[kTCKStages], k_empty[kTCKStages];
   uint64_t v_full[kTCVStages], v_empty[kTCVStages];
   uint64_t s_full[2], s_free[2];
-  uint64_t p_full, pv_done[2], mma_done;  // P V of tile j completes on pv_done[j & 1]
+  uint64_t p_full[2], pv_done[2], mma_done;  // by tile parity: P of tile j is ready, P V of it done
   int2 meta[kTCKStages];  // per K stage: (first key token, valid keys) or (0, -1): no more
   uint32_t tmem_base;
 };
@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(kTCThreads, 2)
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->s_free[s], 4);
     }
-    mbar_init(&bars->p_full, 4);
+    // two of them: a softmax warp may be a tile ahead of another, and its arrival
+    // must not count for the other's tile
+    mbar_init(&bars->p_full[0], 4);
+    mbar_init(&bars->p_full[1], 4);
     mbar_init(&bars->pv_done[0], 1);
     mbar_init(&bars->pv_done[1], 1);
     mbar_init(&bars->mma_done, 1);
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kTCThreads, 2)
       bool ok = mbar_wait(&bars->q_full, 0);
       const uint32_t q_addr = smem_u32(q_s);
       auto issue_pv = [&](uint32_t jj) -> bool {
-        if (!mbar_wait(&bars->p_full, jj & 1)) return false;
+        if (!mbar_wait(&bars->p_full[jj & 1], (jj >> 1) & 1)) return false;
         const int vs = jj % kTCVStages;
         if (!mbar_wait(&bars->v_full[vs], (jj / kTCVStages) & 1)) return false;
         tc_fence_after();
@@ -537,7 +540,7 @@ __global__ void __launch_bounds__(kTCThreads, 2)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->p_full);
+      if (lane == 0) mbar_arrive(&bars->p_full[it & 1]);
     }
     if (!ok) flag_status(p.status, SEER_DEV_TIMEOUT);
     // ---- epilogue: the last P V, then normalise, bf16 out, natural-log lse
