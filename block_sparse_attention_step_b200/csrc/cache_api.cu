@@ -74,31 +74,36 @@ seer_status make_rows_map(const uint16_t* q, const seer_dims* d, int T, int ntok
 
 constexpr int kClusterMax = 8;  // CTAs that join one row's pieces without a partial
 
-// Pieces per row.  As many as fill the SMs' resident CTAs once, up to the 8 a
-// cluster joins (16 sequences x 8 heads, 52 stages of an e4m3 cache: 1 / 2 / 3 /
-// 4 / 8 pieces 30.0 / 27.3 / 27.3 / 35.5 / 39.0 us; a second wave costs each
-// piece's start again).  Past that, partials and a combine (2 us more) once a
-// piece of 8 would still run 10 stages (0.4 us each).  Rows that fill the SMs
-// several times over: no piece above 72 stages, which would run on alone at the
-// end (64 ragged sequences x 8 heads of up to 104 stages: 1 / 2 / 4 pieces 120.8 /
-// 111.7 / 116.1 us; of 66 stages, bf16: 1 / 2 pieces 146 / 156 us).
+// Pieces per row: the number for which the SMs' resident CTAs are through
+// soonest, by waves of CTAs x (a piece's stages + kPieceStart) x (0.6 + 0.4 x the
+// share of CTA slots those waves fill), and kCombineStages where partials need
+// a combine.  A stage of a lone CTA takes 0.41 us; a piece's start and join
+// (launch, three dependent loads, the first copy, the cluster) about 11 of
+// them.  Measured, pieces 1 / 2 / 3 / 4 / 8 (us):
+//   128 rows of 52 stages, e4m3     30.0 / 27.3 / 27.3 / 35.5 / 39.0   rule: 3
+//   256 rows of 58, e4m3            51.2 / 68.8 / 57.9 / 62.9          rule: 1
+//   512 rows of 58, e4m3           117.5 / 106.5 / 105.2 / 110.4       rule: 2
+//   512 ragged rows to 104, int8   118.7 / 110.9 / 112.7 / 116 / 155   rule: 2
+//   512 ragged rows to 66, bf16      146 / 156 / 158 / 160 / 202       rule: 1
+//   1 row of 8, e4m3                 8.3 / 7.1 / 6.5 / 5.4 / 4.9       rule: 8
+constexpr int kPieceStart = 11, kCombineStages = 5;
+
 int32_t pick_splits(const seer_dims* d, int64_t stages, int ctas_per_sm) {
   const int64_t rows = (int64_t)d->batch * d->num_kv_heads;
-  const int64_t fill = (int64_t)num_sms_current() * ctas_per_sm / rows;
-  int64_t s = fill < stages ? fill : stages;
-  if (s > kClusterMax) s = kClusterMax;
-  if (s < 1) s = 1;
-  if (stages >= 10 * kClusterMax) {
-    int64_t clusters = stages / (8 * kClusterMax);
-    if (clusters > fill / kClusterMax) clusters = fill / kClusterMax;
-    if (clusters > kMaxSplits / kClusterMax) clusters = kMaxSplits / kClusterMax;
-    if (clusters >= 2) s = clusters * kClusterMax;
+  const int64_t slots = (int64_t)num_sms_current() * ctas_per_sm;
+  int32_t best = 1;
+  double least = 1e300;
+  for (int32_t s = 1; s <= kMaxSplits; s += s < kClusterMax ? 1 : kClusterMax) {
+    const int64_t waves = (rows * s + slots - 1) / slots;
+    const double fill = (double)(rows * s) / (double)(waves * slots);
+    const double cost = (double)(waves * ((stages + s - 1) / s + kPieceStart)) * (0.6 + 0.4 * fill) +
+                        (s > kClusterMax ? kCombineStages : 0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
   }
-  if (stages > 72 * s) {
-    s = (stages + 71) / 72;
-    if (s > kClusterMax) s = kClusterMax;
-  }
-  return (int32_t)s;
+  return best;
 }
 
 // Stages of 64 tokens that the longest row of a window with sinks can have.
@@ -194,7 +199,9 @@ extern "C" {
 
 int32_t seer_sparse_decode_q8_splits(const seer_dims* d, int32_t k_max) {
   if (check_dims(d) != SEER_OK || k_max < 1) return 1;
-  return pick_splits(d, (int64_t)k_max * (d->block_size / kTileTokens), 3);
+  // resident CTAs per SM: 3, or 2 with more than 8 heads to a group
+  const int per_sm = d->num_q_heads / d->num_kv_heads > 8 ? 2 : 3;
+  return pick_splits(d, (int64_t)k_max * (d->block_size / kTileTokens), per_sm);
 }
 
 int32_t seer_window_decode_splits(const seer_dims* d, int32_t window, int32_t sinks) {
