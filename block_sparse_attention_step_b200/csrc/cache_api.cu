@@ -168,8 +168,10 @@ seer_status cache_decode(const seer_dims* d, const seer_cache_attn_args* a, bool
   p.bs = d->block_size;
   p.max_blocks = d->max_blocks;
   p.k_max = a->k_max;
-  p.window = a->window;
-  p.sinks = a->sinks;
+  // more than a cache can hold sees no more (and keeps positions in 32 bits)
+  const int32_t capacity = d->max_blocks * d->block_size;
+  p.window = a->window < capacity ? a->window : capacity;
+  p.sinks = a->sinks < capacity ? a->sinks : capacity;
   p.S = S;
   p.C = S < kClusterMax ? S : kClusterMax;
   p.num_pages = d->num_pages;
@@ -328,9 +330,15 @@ seer_status seer_window_prefill(const seer_dims* d, const seer_window_prefill_ar
   p.max_blocks = d->max_blocks;
   p.T = a->total_tokens;
   p.max_new = a->max_new;
-  p.window = a->window;
-  p.sinks = a->sinks;
+  // more than a cache can hold sees no more (and keeps positions in 32 bits)
+  const int32_t capacity = d->max_blocks * d->block_size;
+  p.window = a->window < capacity ? a->window : capacity;
+  p.sinks = a->sinks < capacity ? a->sinks : capacity;
   p.ntok = kWPTileRows / p.G;
+  p.v_pool = a->v_pool;
+  p.stride_page = d->stride_page;
+  p.stride_token = d->stride_token;
+  p.stride_head = d->stride_head;
   p.token_inner = d->stride_token < d->stride_head ? 1 : 0;
   p.num_pages = d->num_pages;
   p.scale_log2 = a->softmax_scale * kLog2e;

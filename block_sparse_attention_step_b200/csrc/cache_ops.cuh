@@ -64,13 +64,14 @@ struct WindowPrefillParams {
   const int32_t* cu;  // [B + 1], or nullptr: one token per sequence
   const int32_t* seqlens;
   const int32_t* page_table;
+  const uint16_t* v_pool;
   uint16_t* out;  // [T][Hq][D]
   float* lse;     // optional [Hq][T]
   int32_t* status;
   int B, Hq, Hkv, G, bs, max_blocks, T, max_new, window, sinks;
   int ntok;  // query tokens of a 128-row tile, floor(128 / G)
   int token_inner;
-  int64_t num_pages;
+  int64_t num_pages, stride_page, stride_token, stride_head;
   float scale_log2;
 };
 

@@ -16,8 +16,10 @@
 //     it issues S of tile j + 2 into the same buffer at once (MMAs of one thread
 //     execute in order), so S of tile j + 1 is there when the softmax of tile j
 //     ends;
-//   * warps 2 and 3 zero the V rows of tokens no row of the CTA sees (a zero
-//     weight times a cached NaN would be NaN);
+//   * warps 2 and 3 keep what a row does not see out of its sum (a zero weight
+//     times a cached NaN would be NaN): they zero the V rows of tokens no row of
+//     the CTA sees, and take NaN and inf out of those that only some rows see;
+//     the rows that do see them get them back at the end;
 //   * warps 4-7, one row per thread: read S from tensor memory, exponentiate in
 //     the exp2 domain, write P as bf16 over S.
 // The softmax reference moves only when a row's maximum grows by more than 2^8
@@ -60,6 +62,9 @@ struct WPBars {
   uint32_t tmem_base;
   int b, tile, stop;
   Seq seq;
+  // tokens that some rows see and some do not and whose value row holds a NaN
+  // or inf: bit t - p_min (diagonal), 128 + t - (p_min - window + 1) (window's start)
+  uint32_t odd[8];
 };
 static_assert(sizeof(WPBars) <= 256, "the barriers fit into the alignment slack");
 
@@ -119,13 +124,9 @@ struct WPKeysOf {
   __device__ __forceinline__ int base(int it) const {
     return (it < sink_tiles ? it : first_tile + (it - sink_tiles)) * kWPKeys;
   }
-  // every token of [t, t + len) is seen by some row
-  __device__ __forceinline__ bool covered(int t, int len) const {
-    return t + len - 1 <= p_max && (t + len <= sinks || t > p_min - window ||
-                                    (t < sinks && sinks > p_min - window));
-  }
-  __device__ __forceinline__ bool seen(int t) const {
-    return t <= p_max && (t < sinks || t > p_min - window);
+  // every row sees all of [t, t + len)
+  __device__ __forceinline__ bool whole(int t, int len) const {
+    return t + len - 1 <= p_min && (t > p_max - window || t + len <= sinks);
   }
 };
 
@@ -142,10 +143,45 @@ __device__ __forceinline__ WPKeysOf wp_keys(int p_min, int p_max, int window, in
   return k;
 }
 
+// The top bit of each half of a bf16 pair that is a NaN or inf (exponent all
+// ones), and the pair with those taken as zero.
+__device__ __forceinline__ uint32_t odd_of(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t drop_odd(uint32_t w) {
+  const uint32_t odd = odd_of(w);
+  return w & ~((odd & 0x8000u ? 0xffffu : 0u) | (odd & 0x80000000u ? 0xffff0000u : 0u));
+}
+
+// Adds the NaN and inf elements that were taken out of the value rows of partly
+// seen tokens to the staged bf16 row (swizzled, see the epilogue) of a query
+// that sees them.
+__device__ __noinline__ void add_odd(const WindowPrefillParams& p, const uint32_t* odd, int p_min,
+                                     int b, int h, int pos, uint8_t* row, int swizzle) {
+  for (int bit = 0; bit < 256; ++bit) {
+    if (!(odd[bit >> 5] & (1u << (bit & 31)))) continue;
+    const int t = bit < 128 ? p_min + bit : p_min - p.window + 1 + bit - 128;
+    if (t > pos || (t <= pos - p.window && t >= p.sinks)) continue;
+    const int j = t / p.bs;
+    const int64_t page = page_of(p.page_table, b, j, p.max_blocks);
+    if (page < 0 || page >= p.num_pages) continue;
+    const uint16_t* v = p.v_pool + page * p.stride_page + (int64_t)(t - j * p.bs) * p.stride_token +
+                        (int64_t)h * p.stride_head;
+    for (int e = 0; e < kHeadDim; ++e) {
+      const uint32_t w = v[e];
+      if ((w & 0x7f80u) != 0x7f80u) continue;
+      uint16_t* at = reinterpret_cast<uint16_t*>(row + (((e >> 3) ^ swizzle) << 4)) + (e & 7);
+      *at = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float((uint32_t)*at << 16) +
+                                                     __uint_as_float(w << 16)));
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kWPThreads, 2)
     window_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const WindowPrefillParams p) {
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ WindowPrefillParams p) {
   extern __shared__ uint8_t wp_raw[];
   // 1024-byte aligned data (the 128-byte swizzle atom); the barriers go into
   // the slack in front when there are 256 bytes of it, else behind the data
@@ -219,6 +255,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
         mbar_init(&bars.pv_done[i], 1);
       }
       mbar_init(&bars.mma_done, 1);
+      for (int i = 0; i < 8; ++i) bars.odd[i] = 0u;
       fence_mbar_init();
     }
   } else if (warp == 3) {
@@ -354,9 +391,35 @@ __global__ void __launch_bounds__(kWPThreads, 2)
         flag_status(p.status, SEER_DEV_TIMEOUT);
         break;
       }
-      if (!keys.covered(s0, kWPKeys)) {
+      if (!keys.whole(s0, kWPKeys)) {
+        // 64 threads: 4 rows of 16 pieces at a time
         uint8_t* vd = v_ring + vs * kWPTile + (tid & 7) * 16 + ((tid >> 3) & 1) * kWPBox;
-        auto zero = [&](int lo, int hi) {  // 64 threads: 4 rows of 16 pieces at a time
+        // A token that only some rows see weighs zero in the others, and zero
+        // times NaN or inf is NaN: such elements are taken out here and added
+        // at the end to the rows that do see the token.
+        auto take_out = [&](int lo, int hi, int first_bit) {  // keys [lo, hi) of the tile
+          for (int k0 = lo + (tid >> 4); k0 < hi; k0 += 16) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              v[u] = k0 + 4 * u < hi ? *reinterpret_cast<const uint4*>(vd + (k0 + 4 * u) * 128)
+                                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if ((odd_of(v[u].x) | odd_of(v[u].y) | odd_of(v[u].z) | odd_of(v[u].w)) == 0u) continue;
+              const int key = k0 + 4 * u, bit = first_bit + key;
+              *reinterpret_cast<uint4*>(vd + key * 128) =
+                  make_uint4(drop_odd(v[u].x), drop_odd(v[u].y), drop_odd(v[u].z), drop_odd(v[u].w));
+              atomicOr(&bars.odd[bit >> 5], 1u << (bit & 31));
+            }
+          }
+        };
+        // behind the window's start of some rows (and no sink), ahead of some rows
+        const int w0 = pa - p.window + 1;
+        take_out(max(0, max(keys.sinks, w0) - s0), min(kWPKeys, min(pz - p.window, pa) + 1 - s0),
+                 128 + s0 - w0);
+        take_out(max(0, pa + 1 - s0), min(kWPKeys, pz + 1 - s0), s0 - pa);
+        auto zero = [&](int lo, int hi) {
           for (int key = lo + (tid >> 4); key < hi; key += 4)
             *reinterpret_cast<uint4*>(vd + key * 128) = make_uint4(0u, 0u, 0u, 0u);
         };
@@ -389,7 +452,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       const int s0 = keys.base(it);
       // unless every row sees the whole key tile: this row's keys c, c < hi and
       // (c >= lo or c < sk)
-      if (!(s0 + kWPKeys - 1 <= pa && (s0 > pz - p.window || s0 + kWPKeys <= p.sinks))) {
+      if (!keys.whole(s0, kWPKeys)) {
         const uint64_t seen = live ? below(pos - s0 + 1) & (~below(pos - p.window + 1 - s0) |
                                                             below(p.sinks - s0))
                                    : 0ull;
@@ -492,6 +555,10 @@ __global__ void __launch_bounds__(kWPThreads, 2)
           *reinterpret_cast<uint4*>(stage + r * 256 + (((8 * c2 + e8) ^ (r & 15)) << 4)) = v;
         }
       }
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) odd |= bars.odd[i];
+      if (odd != 0u && live) add_odd(p, bars.odd, pa, b, h, pos, stage + r * 256, r & 15);
       __syncwarp();
       const int r0 = 32 * quarter + (lane >> 4), piece = lane & 15;
 #pragma unroll 4

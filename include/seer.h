@@ -615,9 +615,8 @@ SEER_API seer_status seer_window_decode(const seer_dims *d, const seer_cache_att
  * with t > p - window or t < sinks.  cu_tokens, total_tokens, max_new and the
  * sequences that are left out are those of seer_append_rope; rows that belong
  * to no sequence keep what out and lse hold.  Blocks that no query of the call
- * sees are not looked up.  softmax_scale > 0.  A NaN or inf in the value row of
- * a token that some of the neighbouring queries see reaches those neighbours
- * too (2 * floor(128 / group) query tokens are worked on together). */
+ * sees are not looked up, and what the cache holds in tokens that a query does
+ * not see never reaches its row.  softmax_scale > 0. */
 typedef struct seer_window_prefill_args {
   const uint16_t *q;         /* [T][Hq][D] bf16, 16-byte aligned */
   const uint16_t *k_pool;

@@ -250,7 +250,7 @@ def test_nan_that_a_row_sees_reaches_its_output():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("cache", ["bf16", "e4m3", "int8"])
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (63, 4), (64, 64), (200, 100), (1000, 3), (5000, 0), (17, 5000)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (63, 4), (64, 64), (200, 100), (1000, 3), (5000, 0), (17, 5000), (2 ** 31 - 1, 0), (5, 2 ** 31 - 1)])
 def test_window_decode(cache, window, sinks):
     require_gpu()
     n = window + sinks

@@ -107,14 +107,14 @@ def test_groups(G, Hkv):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (64, 0), (127, 128), (128, 129), (129, 1), (1000, 0), (5000, 64), (300, 300), (40, 5000)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (64, 0), (127, 128), (128, 129), (129, 1), (1000, 0), (5000, 64), (300, 300), (40, 5000), (2 ** 31 - 1, 2 ** 31 - 1)])
 @pytest.mark.parametrize("bs,layout", [(64, "nhd"), (128, "hnd")])
 def test_windows_and_sinks(window, sinks, bs, layout):
     require_gpu()
     past, new = [0, 700, 63, 0], [300, 65, 1, 0]
-    c = make_cache([p + n for p, n in zip(past, new)], 1, bs, "bf16", layout, seed=window + sinks)
+    c = make_cache([p + n for p, n in zip(past, new)], 1, bs, "bf16", layout, seed=(window + sinks) % 1000)
     poison(c, seen_of(c, past, new, window, sinks))
-    q, out, lse, _ = run(c, past, new, 4, window, sinks, seed=window, drop_pages=True)
+    q, out, lse, _ = run(c, past, new, 4, window, sinks, seed=window % 1000, drop_pages=True)
     check(c, past, new, q, out, lse, window, sinks)
 
 
@@ -200,6 +200,40 @@ def test_long_chunk_gives_the_same_bits_every_time():
         seer.seer_window_prefill(d, a)
         assert torch.equal(first, out) and torch.equal(first_lse, lse)
     assert status.item() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks,bs", [(70, 3, 64), (9, 0, 128), (400, 130, 64)])
+def test_odd_values_reach_only_the_queries_that_see_them(window, sinks, bs):
+    """NaN and infinities in keys and values of tokens ahead of some queries, behind the window of others, and in a sink."""
+    require_gpu()
+    past, new, L = 200, 90, 290
+    c = make_cache([L], 1, bs, "bf16", seed=window)
+    g = torch.Generator().manual_seed(window)
+    for t, d, x in ((289, 5, math.nan), (250, 100, math.inf), (215, 3, -math.inf), (201, 64, math.nan), (200 - window + 40, 7, math.inf), (200 - window + 5, 127, math.nan)):
+        c["v"][c["table"][0, t // bs], t % bs, 0, d] = x
+    c["v"][c["table"][0, 270 // bs], 270 % bs, 0] = math.nan
+    c["k"][c["table"][0, 275 // bs], 275 % bs, 0, 3] = math.nan
+    q, out, lse, _ = run(c, [past], [new], 5, window, sinks, seed=window)
+    K, V = values(c, "k"), values(c, "v")
+    t = np.arange(L)
+    pages = c["table"][0].numpy()[t // bs]
+    k, v = K[pages, t % bs, 0], V[pages, t % bs, 0]
+    got, qd, gl = out.double().cpu().numpy(), q.double().cpu().numpy(), lse.double().cpu().numpy()
+    for i in range(new):
+        seen = C.window_seen(past + i, L, window, sinks)
+        for h in range(5):
+            with np.errstate(invalid="ignore"):
+                want, want_lse = C.softmax_attention(qd[i, h], k, v, seen, SCALE)
+            assert np.array_equal(np.isnan(got[i, h]), np.isnan(want)), (i, h)
+            assert np.array_equal(np.isposinf(got[i, h]), np.isposinf(want)) and np.array_equal(np.isneginf(got[i, h]), np.isneginf(want))
+            fine = np.isfinite(want)
+            if fine.any():
+                w = np.exp(k[seen] @ qd[i, h] * SCALE - want_lse)
+                spread = w @ np.abs(np.where(np.isfinite(v[seen]), v[seen], 0))
+                a, b = got[i, h][fine], want[fine]
+                assert (np.abs(a - b) <= 2.0 ** -8 * np.abs(b) + (2.0 ** -8 + 1e-4) * (spread[fine] + np.abs(b))).all()
+            assert np.isnan(gl[h, i]) == np.isnan(want_lse)
 
 
 @pytest.mark.gpu
