@@ -28,9 +28,10 @@
 // A block's K scale multiplies its scores.  Its V scale enters the exponent:
 // with y_t = log2 w_t + log2 vs and a running reference M,
 //   O = sum 2^(y_t - M) code_t,   l = sum 2^(y_t - M) / vs,   out = O / l,
-// so a weight is rounded (to f16, 2^-12) relative to the largest contribution
+// so a weight is rounded (to f16, 2^-11) relative to the largest contribution
 // to O, however far the blocks' scales lie apart.  A scale of 0 (all rows zero)
-// counts as 2^-60 with the codes taken as zero.
+// counts as 2^-60 with the codes taken as zero, which leaves l and O in range for
+// scales of 2^-70 to 2^40 beside it.
 // For a bf16 cache P enters as a bf16 hi + lo pair (2^-17).
 //
 // M moves only when a score exceeds it by more than 2^8 (P then stays below

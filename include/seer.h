@@ -482,8 +482,9 @@ SEER_API seer_status seer_step_workspace_init(const seer_dims *d, int32_t k_max,
  * The types a cache holds its keys and values in.  An 8-bit pool has the
  * layouts of a bf16 pool with one byte per element (strides in elements, all
  * multiples of 16) and two fp32 arrays k_scale, v_scale [num_pages][Hkv]: an
- * element is code * scale of its page and KV head.  Scales are finite and
- * >= 0; 0 says that the page's rows of that head are all zero. */
+ * element is code * scale of its page and KV head.  A scale is 0, which says
+ * that the page's rows of that head are all zero, or a number from 2^-70 to
+ * 2^40 (the decodes take weights and V scales as one fp32 product). */
 #define SEER_CACHE_BF16 0
 #define SEER_CACHE_E4M3 1 /* 8-bit float, 4 exponent and 3 mantissa bits, +-448 */
 #define SEER_CACHE_INT8 2 /* two's complement, -127 .. 127 */
@@ -516,9 +517,11 @@ SEER_API seer_status seer_rope_table(int32_t max_position, int32_t rotary_dim,
  * of one head, a block without earlier rows gets the scale 2^k, the least
  * with amax <= 448 * 2^k (e4m3), or amax / 127 (int8); a block with earlier
  * rows keeps its scale, doubled until amax fits, and its earlier codes are
- * rounded again where it grew.  Codes are round-to-nearest-even of value /
- * scale.  NaN and +-inf are flagged (SEER_DEV_NONFINITE_KV) and stored as NaN
- * (int8: 0) and the largest code.
+ * rounded again where it grew.  Codes are round-to-nearest-even of value
+ * times the scale's fp32 reciprocal.  NaN and +-inf are flagged
+ * (SEER_DEV_NONFINITE_KV) and stored as NaN (int8: 0) and the largest code
+ * (next to nothing but zeros with a scale of at least 2^-60, so that the block
+ * does not read as zero).
  *
  * kbar, if not NULL, receives the pooled keys of every block that got rows:
  * the mean of the block's rows as the cache now holds them (for a bf16 cache
@@ -616,7 +619,8 @@ SEER_API seer_status seer_window_decode(const seer_dims *d, const seer_cache_att
  * sequences that are left out are those of seer_append_rope; rows that belong
  * to no sequence keep what out and lse hold.  Blocks that no query of the call
  * sees are not looked up, and what the cache holds in tokens that a query does
- * not see never reaches its row.  softmax_scale > 0. */
+ * not see never reaches its row.  softmax_scale > 0.  A call that finds
+ * SEER_DEV_TIMEOUT set in *dev_status leaves out and lse as they are. */
 typedef struct seer_window_prefill_args {
   const uint16_t *q;         /* [T][Hq][D] bf16, 16-byte aligned */
   const uint16_t *k_pool;

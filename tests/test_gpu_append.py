@@ -292,6 +292,48 @@ def test_nonfinite_rows_are_flagged_and_bounded(cache):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bs", [64, 128])
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+def test_nonfinite_rows_next_to_zeros_do_not_read_as_zero(cache, bs):
+    """Nothing finite but zeros: the scale is 2^-60, not 0, so NaN stays NaN through a decode,
+    and a later row finds the scale doubled until it fits."""
+    require_gpu()
+    s = setup_case(1, 1, 1, bs, [0], [2], cache=cache, seed=13)
+    page = s["table"][0, 0]
+
+    def append(rows, length):
+        x = rows.cuda()
+        a = seer.append_args(x, x.clone(), s["kp"], s["vp"], s["table"].cuda(), torch.tensor([length], dtype=torch.int32).cuda(),
+                             cu_tokens=torch.tensor([0, len(rows)], dtype=torch.int32).cuda(), max_new=len(rows),
+                             k_scale=s["ks"], v_scale=s["vs"], dev_status=s["status"])
+        seer.seer_append_rope(s["dims"], a)
+        torch.cuda.synchronize()
+        return [values(pool, "nhd")[page, :length, 0] for pool in (s["kp"], s["vp"])]
+
+    first = torch.zeros((2, 1, D)).bfloat16()
+    first[0, 0, 3], first[1, 0, 4], first[1, 0, 5] = float("nan"), float("inf"), float("-inf")
+    top = {"e4m3": 448.0, "int8": 127.0}[cache]
+    for x, scale in zip(append(first, 2), (s["ks"], s["vs"])):
+        assert float(scale[page, 0]) == 2.0 ** -60
+        assert np.isnan(x[0, 3]) if cache == "e4m3" else x[0, 3] == 0
+        assert x[1, 4] == top and x[1, 5] == -top
+        x[0, 3] = x[1, 4] = x[1, 5] = 0
+        assert (x == 0).all()
+    assert s["status"].item() == seer.DEV_NONFINITE_KV
+    if cache == "e4m3":
+        q = torch.ones((1, 1, D)).bfloat16().cuda()
+        out = torch.zeros_like(q)
+        w = seer.window_decode_args(q, s["kp"], s["vp"], s["table"].cuda(), torch.tensor([2], dtype=torch.int32).cuda(), out=out, window=2, sinks=0,
+                                    softmax_scale=0.1, k_scale=s["ks"], v_scale=s["vs"], num_splits=1)
+        seer.seer_window_decode(s["dims"], w)
+        assert out.isnan().all()
+    for x, scale in zip(append(torch.ones((1, 1, D)).bfloat16(), 3), (s["ks"], s["vs"])):
+        step = C.block_scale(cache, 1.0, 2.0 ** -60, True)
+        assert float(scale[page, 0]) == step
+        assert (x[2] == 1.0 / step).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("cache,kbar", [("bf16", False), ("bf16", True), ("e4m3", True)])
 def test_sequences_that_do_not_fit_are_left_out(cache, kbar):
     """A sequence shorter than its new tokens, one longer than its table, one with a bad page, rows
