@@ -33,13 +33,14 @@
 //     cache is bf16 and no pooled keys are wanted.
 // Eight threads take a row, 16 dims each, as two 16-byte chunks that hold
 // whole pairs (chunks i and i + rot/16, or neighbours for interleaved pairs).
-// The row role is a stream: 2 x 16K tokens of 40 + 8 + 8 heads (950 MB both ways)
-// take 176 us, 5.4 TB/s, 0.83 of a plain copy's rate (rows of 128 dims in three
-// strided streams per token; one kernel for both roles' CTAs, since a separate
-// one for the blocks cost 234).  The block role works on each value three times
-// (turn, amax, code) between its loads and stores, with one barrier between: 8 x
-// 2K tokens of 32 + 8 + 8 heads into an int8 cache take 55 us, 4.2 TB/s; a single
-// token per sequence (64) 5.9 us, all of it launch and dependent loads.
+// Bound by HBM where the cache is bf16: 2 x 16K tokens of 40 + 8 + 8 heads with
+// pooled keys (950 MB, q by the row role, k and v by the block role) take 176 us,
+// 5.4 TB/s, 0.83 of a plain copy's rate; a kernel for each role took 234.  With
+// codes the block role touches each value three times (turn, amax, code) between
+// its loads and its stores, a barrier between: 8 ragged chunks of up to 2.5K
+// tokens of 32 + 8 + 8 heads into an int8 cache take 55 us, 4.2 TB/s.  A single
+// token for each of 64 sequences takes 5.9 us, all of it launch and loads that
+// depend on one another.
 #include <cuda_fp16.h>
 
 #include "block_mean.cuh"

@@ -37,6 +37,11 @@
 // M moves only when a score exceeds it by more than 2^8 (P then stays below
 // 256): a vote per tile instead of a maximum over the warp, and no rescaling
 // of O in between.  Bound by HBM: 256 B (bf16: 512) per token and KV head.
+// bf16, 64 sequences x 8 heads, window 4096: 146 us, 6.7 TB/s.  8 bit: 128-byte
+// rows 1 KB apart (token-major pages of 8 heads) are what bounds it; the copies
+// without the math take 25.3 of 27.3 us (16 x 32K tokens, 10 % of the blocks,
+// 109 MB) and 95.6 of 111 us (64 ragged sequences, 485 MB).  One row of 512
+// tokens takes 4.9 us in 8 pieces: launch, three dependent loads, a copy, the join.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 

@@ -199,3 +199,48 @@ def test_two_streams_with_their_own_caches():
         outs.append([x[2] for x in got])
     for x, y in zip(*outs):
         assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_append_prefill_and_decode_far_into_a_pool(cache):
+    """Pages behind 2^32 elements and rows 2^27 elements apart give the bits of near ones (bf16: append, prefill and
+    decode; e4m3: append with pooled keys and decode)."""
+    require_gpu()
+    T, Hq, Hkv, bs, blocks = 40, 4, 1, 64, 2
+    far = (1 << 32) // (bs * Hkv * D) + 5
+    g = torch.Generator().manual_seed(21)
+    packed = torch.randn((T, (Hq + 2 * Hkv) * D), generator=g).bfloat16().cuda()
+    apart = torch.empty((T, 1 << 27), dtype=torch.bfloat16, device="cuda")
+    apart[:, :packed.shape[1]] = packed
+    dtype = torch.bfloat16 if cache == "bf16" else torch.float8_e4m3fn
+    cu, lens = torch.tensor([0, T], dtype=torch.int32).cuda(), torch.tensor([T + 30], dtype=torch.int32).cuda()
+    rope = seer.seer_rope_table(bs * blocks, 128)
+    got = []
+    for pages, table, x in ((4, [1, 2], packed), (far, [far - 1, far - 3], apart[:, :packed.shape[1]])):
+        q, k, v = [y.unflatten(1, (-1, D)) for y in x.split([Hq * D, Hkv * D, Hkv * D], 1)]
+        kp, vp = [torch.zeros((pages, bs, Hkv, D), dtype=torch.uint8 if cache == "e4m3" else dtype, device="cuda").view(dtype) for _ in range(2)]
+        ks = vs = None
+        if cache == "e4m3":
+            ks, vs = torch.zeros((pages, Hkv), device="cuda"), torch.zeros((pages, Hkv), device="cuda")
+        d = seer.make_dims(1, Hq, Hkv, D, bs, blocks, pages)
+        tab = torch.tensor([table], dtype=torch.int32).cuda()
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        qr, kbar = torch.empty((T, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, Hkv, blocks, D), device="cuda")
+        seer.seer_append_rope(d, seer.append_args(k, v, kp, vp, tab, lens, q=q, q_out=qr, rope=rope, cu_tokens=cu, max_new=T, k_scale=ks, v_scale=vs,
+                                                  kbar=kbar if cache == "e4m3" else None, dev_status=status))
+        res = [qr, kbar] + [p.view(torch.uint8 if cache == "e4m3" else torch.int16)[table] for p in (kp, vp)]
+        if cache == "bf16":
+            out, lse = torch.zeros_like(qr), torch.zeros((Hq, T), device="cuda")
+            seer.seer_window_prefill(d, seer.window_prefill_args(qr, kp, vp, tab, lens, window=25, sinks=2, softmax_scale=SCALE, out=out, cu_tokens=cu, max_new=T,
+                                                                 lse_out=lse, dev_status=status))
+            res += [out, lse]
+        one = torch.zeros((1, Hq, D), dtype=torch.bfloat16, device="cuda")
+        seer.seer_window_decode(d, seer.window_decode_args(qr[-1:].contiguous(), kp, vp, tab, lens, window=60, sinks=1, num_splits=2, softmax_scale=SCALE,
+                                                           out=one, k_scale=ks, v_scale=vs, dev_status=status))
+        got.append(res + [one, status])
+        torch.cuda.synchronize()
+        del kp, vp
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][-1].item() == 0 and got[0][-2].abs().max() > 0
