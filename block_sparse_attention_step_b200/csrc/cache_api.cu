@@ -346,7 +346,7 @@ seer_status seer_window_prefill(const seer_dims* d, const seer_window_prefill_ar
   SEER_TRY(make_rows_map(a->q, d, p.T, p.ntok, &tq));
   SEER_TRY(make_kv_map(a->k_pool, d, p.token_inner, &tk));
   SEER_TRY(make_kv_map(a->v_pool, d, p.token_inner, &tv));
-  SEER_CUDA(run_window_prefill(tq, tk, tv, p, stream));
+  SEER_CUDA(run_window_prefill(tq, tk, tv, p, num_sms_current(), stream));
   return SEER_OK;
 }
 

@@ -76,7 +76,7 @@ struct WindowPrefillParams {
 };
 
 cudaError_t run_window_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const WindowPrefillParams& p, cudaStream_t stream);
+                               const WindowPrefillParams& p, int num_sms, cudaStream_t stream);
 
 cudaError_t run_cache_decode(const CUtensorMap& tk, const CUtensorMap& tv,
                              const CacheDecodeParams& p, int cache, bool window,

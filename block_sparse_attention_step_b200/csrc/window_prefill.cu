@@ -27,15 +27,22 @@
 // unrounded weights.  Two CTAs run out of step, so one's MMAs, the other's
 // softmax and either one's start and end overlap.  Bound by the MMAs: at N 64
 // reading Q (4 KB) and K (2 KB) of each K step at 128 B per cycle takes 49
-// cycles for 32 cycles of products.  8K prompt (40/8 heads, window 2048, 301
+// cycles for 32 cycles of products.
+// Where there are too few row tiles for the SMs (a short chunk behind a long
+// context) the CTAs of a cluster take a part of a tile's keys each and join their
+// states (O, maximum, sum in fp32) over distributed shared memory.  8K prompt (40/8 heads, window 2048, 301
 // GFLOP): 363 us in a loop at the power limit, 333 in a burst (903 TFLOP/s); ragged
 // chunks of 129 to 2050 tokens (32/8 heads, window 1000): 98 to 104.  N 128 with two Q
 // tiles per CTA and one CTA per SM took 364 to 398, and 17 us instead of 10.7 on a
 // chunk of 77 tokens.
+#include <cooperative_groups.h>
+
 #include "cache_ops.cuh"
 #include "packed.cuh"
 #include "ragged.cuh"
 #include "tcgen05.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace seer {
 
@@ -47,6 +54,7 @@ constexpr int kWPTile = 2 * kWPBox;           // a K or V tile
 constexpr int kWPHalf = kWPRows * 128;        // 64 dims x 128 rows of q: 16 KB
 constexpr int kWPKStages = 3, kWPVStages = 2;
 constexpr size_t kWPData = 2 * kWPHalf + (size_t)(kWPKStages + kWPVStages) * kWPTile;  // 112 KB
+constexpr int kWPCluster = 8;                 // pieces of a tile's keys, at most
 constexpr size_t kWPSmem = kWPData + 1024;    // alignment slack, which holds the barriers too
 constexpr float kWPSlack = 8.f;
 // One pair in so many takes its 2^y from the FMA pipe.  8K prompt (40/8 heads,
@@ -65,6 +73,7 @@ struct WPBars {
   uint64_t mma_done;
   uint32_t tmem_base;
   int b, tile, stop;
+  int done;  // this CTA's part of the outputs is whole
   Seq seq;
   // tokens that some rows see and some do not and whose value row holds a NaN
   // or inf: bit t - p_min (diagonal), 128 + t - (p_min - window + 1) (window's start)
@@ -124,8 +133,10 @@ __device__ __forceinline__ uint64_t below(int n) {
 struct WPKeysOf {
   int p_min, p_max, window, sinks, L;
   int sink_tiles, first_tile, n;  // tile numbers 0 .. sink_tiles - 1, then first_tile ..
+  int lo;                         // first of them that is this CTA's
 
   __device__ __forceinline__ int base(int it) const {
+    it += lo;
     return (it < sink_tiles ? it : first_tile + (it - sink_tiles)) * kWPKeys;
   }
   // every row sees all of [t, t + len)
@@ -144,6 +155,7 @@ __device__ __forceinline__ WPKeysOf wp_keys(int p_min, int p_max, int window, in
   k.sink_tiles = ceil_div_i(k.sinks, kWPKeys);
   k.first_tile = max(k.sink_tiles, max(0, p_min - window + 1) / kWPKeys);
   k.n = k.sink_tiles + max(0, p_max / kWPKeys + 1 - k.first_tile);
+  k.lo = 0;
   return k;
 }
 
@@ -181,6 +193,35 @@ __device__ __noinline__ void add_odd(const WindowPrefillParams& p, const uint32_
   }
 }
 
+// The same for four values (dims 4 * c4 ..) of a split row; odd: every piece's bits.
+__device__ __noinline__ float4 add_odd4(const WindowPrefillParams& p, const uint32_t* odd, int p_min,
+                                        int b, int h, int pos, int c4, float4 v) {
+  for (int bit = 0; bit < 256; ++bit) {
+    if (!(odd[bit >> 5] & (1u << (bit & 31)))) continue;
+    const int t = bit < 128 ? p_min + bit : p_min - p.window + 1 + bit - 128;
+    if (t > pos || (t <= pos - p.window && t >= p.sinks)) continue;
+    const int j = t / p.bs;
+    const int64_t page = page_of(p.page_table, b, j, p.max_blocks);
+    if (page < 0 || page >= p.num_pages) continue;
+    const uint2 w = *reinterpret_cast<const uint2*>(p.v_pool + page * p.stride_page +
+                                                    (int64_t)(t - j * p.bs) * p.stride_token +
+                                                    (int64_t)h * p.stride_head + 4 * c4);
+    const uint32_t e[4] = {w.x << 16, w.x & 0xffff0000u, w.y << 16, w.y & 0xffff0000u};
+    float* y = &v.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((e[i] & 0x7f800000u) == 0x7f800000u) y[i] += __uint_as_float(e[i]);
+  }
+  return v;
+}
+
+// A split row tile's partial state in a CTA's shared memory: O [128][128] fp32
+// (16-byte pieces swizzled by row), then m, l of each row.
+constexpr int kWPPartML = kWPRows * kHeadDim * 4;
+
+// C > 1: the C CTAs of a cluster share the tile's rows and take a part of its key
+// tiles each; their states are joined over distributed shared memory.
+template <int C>
 __global__ void __launch_bounds__(kWPThreads, 2)
     window_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
@@ -198,8 +239,9 @@ __global__ void __launch_bounds__(kWPThreads, 2)
   uint8_t* v_ring = k_ring + kWPKStages * kWPTile;
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int h = (int)blockIdx.x % p.Hkv;
-  const int item = (int)blockIdx.x / p.Hkv;
+  const int piece = (int)blockIdx.x % C;
+  const int h = (int)blockIdx.x / C % p.Hkv;
+  const int item = (int)blockIdx.x / C / p.Hkv;
 
   // ---- which sequence and which of its token tiles (warp 0); meanwhile
   // tensor memory (warp 1), barriers (warp 2), tensor maps (warp 3)
@@ -260,6 +302,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       }
       mbar_init(&bars.mma_done, 1);
       for (int i = 0; i < 8; ++i) bars.odd[i] = 0u;
+      bars.done = 1;
       fence_mbar_init();
     }
   } else if (warp == 3) {
@@ -288,8 +331,12 @@ __global__ void __launch_bounds__(kWPThreads, 2)
   const int t0 = bars.tile * p.ntok;                       // first query token of the CTA
   const int last = min(t0 + p.ntok, seq.n) - 1;            // last query token
   const int pa = past + t0, pz = past + last;              // their positions
-  const WPKeysOf keys = wp_keys(pa, pz, p.window, p.sinks, seq.L);
-  const int nt = bars.stop ? 0 : keys.n;
+  WPKeysOf keys = wp_keys(pa, pz, p.window, p.sinks, seq.L);
+  int nt = bars.stop ? 0 : keys.n;
+  if constexpr (C > 1) {
+    keys.lo = (int)((int64_t)piece * nt / C);
+    nt = (int)((int64_t)(piece + 1) * nt / C) - keys.lo;
+  }
 
   if (warp == 0) {
     // ================================================================ copies
@@ -538,7 +585,29 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       if (!have) flag_status(p.status, SEER_DEV_TIMEOUT);
     }
     tc_fence_after();
-    if (have) {
+    if constexpr (C > 1) {
+      // this piece's state; a piece without key tiles adds nothing
+      if (bars.stop || (nt > 0 && !have)) {
+        bars.done = 0;
+      } else {
+#pragma unroll 1
+        for (int c2 = 0; c2 < 4; ++c2) {
+          uint32_t o[32];
+          if (nt > 0) {
+            __syncwarp();
+            tmem_ld32(o_addr + 32 * c2, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+#pragma unroll
+          for (int e4 = 0; e4 < 8; ++e4)
+            *reinterpret_cast<uint4*>(data + r * (kHeadDim * 4) + (((8 * c2 + e4) ^ (r & 31)) << 4)) =
+                make_uint4(o[4 * e4], o[4 * e4 + 1], o[4 * e4 + 2], o[4 * e4 + 3]);
+        }
+        *reinterpret_cast<float2*>(data + kWPPartML + 8 * r) = make_float2(m_ref, l);
+      }
+    } else if (have) {
       // rows through shared memory (q, which no MMA reads any more), so that a
       // row leaves as one 256-byte piece
       const int qh = h * p.G + r % p.G;
@@ -585,32 +654,155 @@ __global__ void __launch_bounds__(kWPThreads, 2)
     tc_fence_after();
     tmem_dealloc(tmem, kWPCols);
   }
+  if constexpr (C > 1) {
+    // ---- join: each CTA takes every C-th row, four dims of it a thread
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const uint8_t* part[C];
+    int whole = 1;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int q = 0; q < C; ++q) {
+      part[q] = cluster.map_shared_rank(data, q);
+      const WPBars* at = cluster.map_shared_rank(&bars, q);
+      whole &= at->done;
+      odd |= at->odd[lane & 7];
+    }
+    const bool any_odd = __any_sync(0xffffffffu, odd != 0u);
+    constexpr int kRows = kWPCluster / C;  // rows whose loads are in flight together
+    const int end = whole ? min(p.ntok, seq.n - t0) * p.G : 0;
+    for (int r0 = piece + C * kRows * warp; r0 < end; r0 += C * kRows * (kWPThreads / 32)) {
+      float2 ml[kRows][C];
+      float4 o[kRows][C];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = min(r0 + C * i, kWPRows - 1);
+#pragma unroll
+        for (int q = 0; q < C; ++q) {
+          ml[i][q] = *reinterpret_cast<const float2*>(part[q] + kWPPartML + 8 * r);
+          o[i][q] = *reinterpret_cast<const float4*>(part[q] + r * (kHeadDim * 4) +
+                                                     ((lane ^ (r & 31)) << 4));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + C * i;
+        if (r >= end) break;
+        const int tk = r / p.G, qh = h * p.G + r - tk * p.G;
+        float m = ml[i][0].x;
+#pragma unroll
+        for (int q = 1; q < C; ++q) m = fmaxf(m, ml[i][q].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < C; ++q) {
+          const float f = fast_exp2(ml[i][q].x - ref);
+          l = fmaf(ml[i][q].y, f, l);
+          v.x = fmaf(o[i][q].x, f, v.x);
+          v.y = fmaf(o[i][q].y, f, v.y);
+          v.z = fmaf(o[i][q].z, f, v.z);
+          v.w = fmaf(o[i][q].w, f, v.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        if (any_odd) {
+          uint32_t bits[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) bits[k] = __shfl_sync(0xffffffffu, odd, k);
+          v = add_odd4(p, bits, pa, b, h, pa + tk, lane, v);
+          __syncwarp();
+        }
+        const int64_t row = seq.first + t0 + tk;
+        *reinterpret_cast<uint2*>(p.out + (row * p.Hq + qh) * kHeadDim + 4 * lane) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        if (lane == 0 && p.lse != nullptr)
+          p.lse[(int64_t)qh * p.T + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+    }
+    // nobody leaves while its state is being read
+    cluster.sync();
+  }
+}
+
+template <int C>
+static cudaError_t launch_window_prefill(const CUtensorMap& tq, const CUtensorMap& tk,
+                                         const CUtensorMap& tv, const WindowPrefillParams& p,
+                                         int64_t rows, cudaStream_t stream) {
+  static std::atomic<uint64_t> smem_set{0};
+  cudaError_t e = ensure_smem_limit(window_prefill_kernel<C>, smem_set);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * C));
+  cfg.blockDim = dim3(kWPThreads);
+  cfg.dynamicSmemBytes = kWPSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, window_prefill_kernel<C>, tq, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+// CTAs per row tile: the C in 1, 2, 4, 8 with the least
+//   key tiles of a piece x (1, or 1.3 where SMs hold two CTAs)
+//     + for C > 1 a join of 1 + 3 x the share of the 128 rows in use
+// (in tiles, 0.65 to 1 us), as long as all CTAs are resident at once with a few
+// places to spare for clusters that do not fit a GPC's rest.  Measured, C = 1 / 2 / 4 / 8 (us):
+//     1 row tile of 4 rows, 3 key tiles    6.9 /  6.9 /  6.0 /  6.2   rule: 4
+//     1 row tile of 4 rows, 65 key tiles  48.0 / 27.6 / 16.7 / 11.6   rule: 8
+//     3 row tiles, 7 key tiles            10.7 / 10.9 /  8.9 /  8.4   rule: 8
+//    32 row tiles, 17                     20.9 / 17.3 / 14.3 / 14.4   rule: 8
+//    35 row tiles, 17                     21.1 / 17.2 / 13.7 / 22.2   rule: 4
+//    60 row tiles, 7                      12.2 / 13.0 / 12.9 / 24.0   rule: 4
+//    64 row tiles, 33                     38.0 / 26.4 / 19.7 / 32.3   rule: 4
+//    74 row tiles, 17                     18.2 / 15.9 / 24.6 / 36.9   rule: 2
+//   128 row tiles, 33                     39.5 / 27.4 / 36.5 / 61.8   rule: 2
+//   148 row tiles, 17                     18.9 / 19.6 / 38.5 / 64.1   rule: 1
+static int pick_pieces(int64_t row_tiles, int64_t keys, int live_rows, int num_sms) {
+  const double join = 1.0 + 3.0 * live_rows / kWPRows;
+  int best = 1;
+  double least = (double)keys;
+  for (int c = 2; c <= kWPCluster && row_tiles * c <= 2 * num_sms - 4 * c; c *= 2) {
+    const double tile = row_tiles * c <= num_sms ? 1.0 : 1.3;
+    const double cost = tile * (double)((keys + c - 1) / c) + join;
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  return best;
 }
 
 cudaError_t run_window_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const WindowPrefillParams& p, cudaStream_t stream) {
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = ensure_smem_limit(window_prefill_kernel, smem_set);
-  if (e != cudaSuccess) return e;
+                               const WindowPrefillParams& p, int num_sms, cudaStream_t stream) {
   // token tiles: T / ntok and one more for each sequence's ragged end, but no
   // more than every sequence at max_new
   int64_t tiles = p.B * (((int64_t)p.max_new + p.ntok - 1) / p.ntok);
   const int64_t by_rows = p.T / p.ntok + p.B;
   if (by_rows < tiles) tiles = by_rows;
-  if (tiles * p.Hkv > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.Hkv));
-  cfg.blockDim = dim3(kWPThreads);
-  cfg.dynamicSmemBytes = kWPSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, window_prefill_kernel, tq, tk, tv, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  const int64_t rows = tiles * p.Hkv;
+  const int ntok = p.ntok < p.max_new ? p.ntok : p.max_new;  // in use
+  // key tiles that a row tile can have
+  int64_t keys = ((int64_t)p.sinks + kWPKeys - 1) / kWPKeys +
+                 ((int64_t)p.window + ntok - 2) / kWPKeys + 2;
+  const int64_t most = (int64_t)p.max_blocks * p.bs / kWPKeys;
+  if (keys > most) keys = most;
+  const int C = pick_pieces(rows, keys, ntok * p.G, num_sms);
+  if (rows * C > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  switch (C) {
+    case 1: return launch_window_prefill<1>(tq, tk, tv, p, rows, stream);
+    case 2: return launch_window_prefill<2>(tq, tk, tv, p, rows, stream);
+    case 4: return launch_window_prefill<4>(tq, tk, tv, p, rows, stream);
+    default: return launch_window_prefill<8>(tq, tk, tv, p, rows, stream);
+  }
 }
 
 }  // namespace seer

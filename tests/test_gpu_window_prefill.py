@@ -237,6 +237,52 @@ def test_odd_values_reach_only_the_queries_that_see_them(window, sinks, bs):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hkv", [4, 12, 30, 80])
+@pytest.mark.parametrize("window,sinks", [(600, 70), (200, 0)])
+def test_keys_shared_by_the_ctas_of_a_cluster(Hkv, window, sinks):
+    """Few row tiles: their keys are split over 8, 4 or 2 CTAs; many: one CTA each.  Some pieces hold keys
+    that only some rows see, some none at all (the sequence of one token and its neighbours)."""
+    require_gpu()
+    past, new = [700, 0, 63], [40, 130, 1]
+    c = make_cache([p + n for p, n in zip(past, new)], Hkv, 64, "bf16", seed=Hkv)
+    poison(c, seen_of(c, past, new, window, sinks))
+    q, out, lse, (d, a) = run(c, past, new, Hkv, window, sinks, seed=Hkv, drop_pages=True)
+    check(c, past, new, q, out, lse, window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks,bs", [(70, 3, 64), (9, 0, 128), (400, 130, 64)])
+def test_odd_values_in_one_piece_and_in_many(window, sinks, bs):
+    """The same keys, values and queries as one KV head (keys split over a cluster) and as 100 of them (one CTA for
+    each row tile): NaN and inf in the same places, the rest within both roundings."""
+    require_gpu()
+    past, new, L = 200, 90, 290
+    c = make_cache([L], 1, bs, "bf16", seed=window)
+    for t, d, x in ((289, 5, math.nan), (250, 100, math.inf), (215, 3, -math.inf), (200 - window + 40, 7, math.inf), (200 - window + 5, 127, math.nan)):
+        c["v"][c["table"][0, t // bs], t % bs, 0, d] = x
+    c["v"][c["table"][0, 270 // bs], 270 % bs, 0] = math.nan
+    q, few, few_lse, (d, _) = run(c, [past], [new], 5, window, sinks, seed=window)
+    H, T = 100, q.shape[0]
+    d.num_kv_heads, d.num_q_heads = H, 5 * H
+    d.stride_page, d.stride_token, d.stride_head = bs * H * D, H * D, D
+    kp, vp = [on_gpu(c, x).repeat(1, 1, H, 1).contiguous() for x in "kv"]
+    qq = q.repeat(1, H, 1).contiguous()
+    out, lse = torch.empty_like(qq), torch.empty((5 * H, T), device="cuda")
+    cu = torch.tensor([0, new], dtype=torch.int32).cuda()
+    seer.seer_window_prefill(d, seer.window_prefill_args(qq, kp, vp, c["table"].cuda(), torch.tensor([L], dtype=torch.int32).cuda(), cu_tokens=cu, max_new=new,
+                                                         window=window, sinks=sinks, softmax_scale=SCALE, out=out, lse_out=lse))
+    a, b = few[:new].float(), out[:new].float()
+    for h in range(0, 5 * H, 5):
+        x = b[:, h:h + 5]
+        assert torch.equal(x.isnan(), a.isnan()) and torch.equal(x.isposinf(), a.isposinf()) and torch.equal(x.isneginf(), a.isneginf())
+        assert torch.equal(x, b[:, :5]) or torch.equal(x.nan_to_num(9.0), b[:, :5].nan_to_num(9.0))
+    fine = a.isfinite()
+    # both round their weights and outputs to bf16: 2 (2^-8 + 2^-8) of the largest value
+    assert (a - b[:, :5])[fine].abs().max() <= 4 * 2.0 ** -8 * vp.float()[vp.isfinite()].abs().max()
+    assert (few_lse[:, :new] - lse[:5, :new]).abs().max() <= 1e-4
+
+
+@pytest.mark.gpu
 def test_sequences_that_do_not_fit_are_left_out():
     require_gpu()
     past, new = [10, 0, 70], [9, 20, 3]
