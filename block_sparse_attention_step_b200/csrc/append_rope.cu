@@ -34,12 +34,12 @@
 // Eight threads take a row, 16 dims each, as two 16-byte chunks that hold
 // whole pairs (chunks i and i + rot/16, or neighbours for interleaved pairs).
 // Bound by HBM where the cache is bf16: 2 x 16K tokens of 40 + 8 + 8 heads with
-// pooled keys (950 MB, q by the row role, k and v by the block role) take 176 us,
-// 5.4 TB/s, 0.83 of a plain copy's rate; a kernel for each role took 234.  With
-// codes the block role touches each value three times (turn, amax, code) between
-// its loads and its stores, a barrier between: 8 ragged chunks of up to 2.5K
-// tokens of 32 + 8 + 8 heads into an int8 cache take 55 us, 4.2 TB/s.  A single
-// token for each of 64 sequences takes 5.9 us, all of it launch and loads that
+// pooled keys (950 MB, q by the row role, k and v by the block role) take 156 us,
+// 6.1 TB/s, 0.94 of a plain copy's rate; a kernel for each role took 234.  With
+// codes a block's CTA loads, reduces and stores in turn and two of them fill an
+// SM: 8 ragged chunks of up to 2.5K tokens of 32 + 8 + 8 heads into an int8 cache
+// take 53 us, 4.4 TB/s (26 without q, whose rows stream at 6.2 TB/s).  A single
+// token for each of 64 sequences takes 5.8 us, all of it launch and loads that
 // depend on one another.
 #include <cuda_fp16.h>
 
@@ -52,6 +52,7 @@ namespace seer {
 
 constexpr int kRowThreads = 8;      // threads per 128-dim row
 constexpr int kRowTileRows = 384;   // rows of a row-role tile, about
+constexpr int kRowTokens = 16;      // its tokens, a multiple of this (the larger CTA's warps)
 constexpr int kMaxTileTokens = 128;
 
 // ------------------------------------------------------------- 8-bit codes
@@ -61,8 +62,12 @@ struct Code8;
 template <>
 struct Code8<SEER_CACHE_E4M3> {
   static constexpr float kMax = 448.f;
-  // four values (already divided by the scale) to four codes
-  static __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  // four values (already divided by the scale) to four codes; odd: some may be
+  // NaN or inf
+  static __device__ __forceinline__ uint32_t pack4(uint64_t ab, uint64_t cd, bool odd) {
+    float a, b, c, d;
+    unpack2(ab, a, b);
+    unpack2(cd, c, d);
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
@@ -94,8 +99,21 @@ struct Code8<SEER_CACHE_INT8> {
   static __device__ __forceinline__ uint32_t code(float x) {
     return (uint32_t)max(-127, min(127, __float2int_rn(x))) & 0xffu;
   }
-  static __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-    return code(a) | (code(b) << 8) | (code(c) << 16) | (code(d) << 24);
+  static __device__ __forceinline__ uint32_t pack4(uint64_t ab, uint64_t cd, bool odd) {
+    float a, b, c, d;
+    if (odd) {
+      unpack2(ab, a, b);
+      unpack2(cd, c, d);
+      return code(a) | (code(b) << 8) | (code(c) << 16) | (code(d) << 24);
+    }
+    // |x| <= 127 (and a rounding): 1.5 * 2^23 + x rounds x to the nearest integer,
+    // ties to even, whose two's complement is the sum's low byte (converting
+    // instructions run at a quarter of the rate)
+    const uint64_t magic = pack2(12582912.f, 12582912.f);
+    unpack2(add2(ab, magic), a, b);
+    unpack2(add2(cd, magic), c, d);
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
   }
   static __device__ __forceinline__ void unpack4(uint32_t w, float (&x)[4]) {
 #pragma unroll
@@ -525,6 +543,18 @@ __device__ __forceinline__ void block_role(const AppendParams& p, const Touched&
       }
     }
   }
+  int at_row[2] = {0, 0};  // the rotation's table rows, fetched behind the copies
+  if (sl.turned0 || sl.turned1) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (live[u]) {
+        at_row[u] = rope_row(p, (int)t0 + u * kGroups, base + g + u * kGroups);
+        const float* row = p.rope + (int64_t)at_row[u] * p.rot + 4 * (p.interleaved ? sl.c0 : 2 * sl.c0);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(row));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(row + (p.rot >> 1)));
+      }
+    }
+  }
   cp_async_wait();
 
   float key_scale = 1.f;
@@ -535,8 +565,7 @@ __device__ __forceinline__ void block_role(const AppendParams& p, const Touched&
       widen8(kh[u * kNext + sl.c0], x[u]);
       widen8(kh[u * kNext + sl.c1], x[u] + 8);
       if (sl.turned0 || sl.turned1)
-        turn16(p, sl, load_turn(p, sl, rope_row(p, (int)t0 + u * kGroups, base + g + u * kGroups)),
-               x[u]);
+        turn16(p, sl, load_turn(p, sl, at_row[u]), x[u]);
     }
   }
   uint8_t* kd = kp + g * row_bytes;  // row g of the page
@@ -606,19 +635,18 @@ __device__ __forceinline__ void block_role(const AppendParams& p, const Touched&
     key_scale = scale_k;
     const float inv_k = scale_k > 0.f ? __frcp_rn(scale_k) : 0.f;
     const float inv_v = scale_v > 0.f ? __frcp_rn(scale_v) : 0.f;
-    auto code8 = [](const float* y, float f) {
+    auto code8 = [](const float* y, float f, bool odd) {
       const uint64_t f2 = pack2(f, f);
-      float z[8];
+      uint64_t z[4];
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), f2), z[e], z[e + 1]);
-      return make_uint2(Code8<CACHE>::pack4(z[0], z[1], z[2], z[3]),
-                        Code8<CACHE>::pack4(z[4], z[5], z[6], z[7]));
+      for (int e = 0; e < 4; ++e) z[e] = mul2(pack2(y[2 * e], y[2 * e + 1]), f2);
+      return make_uint2(Code8<CACHE>::pack4(z[0], z[1], odd), Code8<CACHE>::pack4(z[2], z[3], odd));
     };
     auto recode = [&](uint2 w, float f) {
       float y[8];
       Code8<CACHE>::unpack4(w.x, *reinterpret_cast<float(*)[4]>(y));
       Code8<CACHE>::unpack4(w.y, *reinterpret_cast<float(*)[4]>(y + 4));
-      return code8(y, f);
+      return code8(y, f, true);
     };
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -630,8 +658,8 @@ __device__ __forceinline__ void block_role(const AppendParams& p, const Touched&
         float y[16];
         widen8(vh[u * kNext + sl.c0], y);
         widen8(vh[u * kNext + sl.c1], y + 8);
-        const uint2 k0 = code8(x[u], inv_k), k1 = code8(x[u] + 8, inv_k);
-        const uint2 v0 = code8(y, inv_v), v1 = code8(y + 8, inv_v);
+        const uint2 k0 = code8(x[u], inv_k, odd_k), k1 = code8(x[u] + 8, inv_k, odd_k);
+        const uint2 v0 = code8(y, inv_v, odd_v), v1 = code8(y + 8, inv_v, odd_v);
         if (sl.c1 == sl.c0 + 1) {  // neighbouring chunks: 16 codes at once
           *reinterpret_cast<uint4*>(ku + sl.c0) = make_uint4(k0.x, k0.y, k1.x, k1.y);
           *reinterpret_cast<uint4*>(vu + sl.c0) = make_uint4(v0.x, v0.y, v1.x, v1.y);
@@ -672,18 +700,28 @@ __device__ __forceinline__ void block_role(const AppendParams& p, const Touched&
         a.w += __uint_as_float(w.y & 0xffff0000u);
       }
     } else {
-      // sums of at most 128 codes are exact (multiples of 2^-9 below 2^16), so
+      // sums of at most 128 codes are exact (e4m3: multiples of 2^-9 below 2^16), so
       // the scale is applied once
       a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int t = warp; t < end; t += kPoolWarps) {
-        float y[4];
-        // dims 4 lane .. 4 lane + 3: half of the codes in the first half of chunk lane / 2
-        Code8<CACHE>::unpack4(
-            reinterpret_cast<const uint32_t*>(sh.keys)[t * 64 + (lane >> 1) * 4 + (lane & 1)], y);
-        a.x += y[0];
-        a.y += y[1];
-        a.z += y[2];
-        a.w += y[3];
+      // dims 4 lane .. 4 lane + 3: half of the codes in the first half of chunk lane / 2
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(sh.keys) + (lane >> 1) * 4 + (lane & 1);
+      if constexpr (CACHE == SEER_CACHE_INT8) {
+        int n[4] = {0, 0, 0, 0};
+        for (int t = warp; t < end; t += kPoolWarps) {
+          const int x4 = (int)w[t * 64];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) n[e] = __dp4a(x4, 1 << (8 * e), n[e]);
+        }
+        a = make_float4((float)n[0], (float)n[1], (float)n[2], (float)n[3]);
+      } else {
+        for (int t = warp; t < end; t += kPoolWarps) {
+          float y[4];
+          Code8<CACHE>::unpack4(w[t * 64], y);
+          a.x += y[0];
+          a.y += y[1];
+          a.z += y[2];
+          a.w += y[3];
+        }
       }
     }
     *reinterpret_cast<float4*>(sh.part + warp * kHeadDim + 4 * lane) = a;
@@ -700,9 +738,13 @@ __global__ void __launch_bounds__(BS * 4, BS == 64 ? 4 : 2) append_blocks_kernel
   extern __shared__ __align__(16) uint8_t ap_raw[];
   pdl_wait();
   pdl_launch_dependents();
-  const int n_blk = p.items * (p.Hkv / p.heads);
-  const int c = (int)blockIdx.x;
-  if (c < n_blk) {
+  // the block CTAs, spread evenly over the grid: they wait for loads, barriers and
+  // arithmetic in turn while the row CTAs stream (2 x 16K prompt 156 us, all
+  // of them first 164, last 160; int8 chunks alike)
+  const int before = (int)((uint64_t)blockIdx.x * p.block_share >> 32);
+  const bool is_block = (int)((uint64_t)(blockIdx.x + 1) * p.block_share >> 32) > before;
+  if (is_block) {
+    const int c = before;
     BlockShared<BS>& sh = *reinterpret_cast<BlockShared<BS>*>(ap_raw);
     const int per_block = p.Hkv / p.heads;  // CTAs of one block
     const Touched where = find_block(p, c / per_block);
@@ -712,7 +754,7 @@ __global__ void __launch_bounds__(BS * 4, BS == 64 ? 4 : 2) append_blocks_kernel
       block_role<BS, CACHE>(p, where, (c % per_block) * p.heads + i, sh);
     }
   } else {
-    row_role(p, c - n_blk, *reinterpret_cast<RowShared*>(ap_raw));
+    row_role(p, (int)blockIdx.x - before, *reinterpret_cast<RowShared*>(ap_raw));
   }
 }
 
@@ -760,13 +802,15 @@ cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t
     // a warp's share of a token: all its rows, or a part of them where there
     // are too few tokens to keep the SMs busy; a CTA's tile: some kRowTileRows
     // rows (its start -- sequences, lengths, pages, three dependent loads -- costs
-    // as much as some 100 rows: 2 x 16K prompt with 56 rows a token, tiles of
-    // 128 / 384 / 1024 rows 194 / 177 / 187 us)
+    // as much as some 100 rows), in whole rounds of its warps: 2 x 16K prompt, tiles
+    // of 4 / 8 / 9 / 12 / 16 / 24 tokens of 40 rows 189 / 161 / 178 / 167 / 163 / 168 us
+    // (before the roles were spread, see append_blocks_kernel)
     int64_t seg = (32 * (int64_t)num_sms + p.T - 1) / p.T;
     if (seg > (R + 3) / 4) seg = (R + 3) / 4;
     p.segment_rows = (int)(((R + seg - 1) / seg + 3) / 4 * 4);
     p.segments = (R + p.segment_rows - 1) / p.segment_rows;
-    p.tile_tokens = p.segments > 1 ? 8 / p.segments : kRowTileRows / R;
+    p.tile_tokens = p.segments > 1 ? 8 / p.segments
+                                     : (kRowTileRows / R + kRowTokens - 1) / kRowTokens * kRowTokens;
     if (p.tile_tokens < 1) p.tile_tokens = 1;
     if (p.tile_tokens > kMaxTileTokens) p.tile_tokens = kMaxTileTokens;
     tiles = ((int64_t)p.T + p.tile_tokens - 1) / p.tile_tokens;
@@ -786,6 +830,9 @@ cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t
     if (p.Hkv % hc == 0) p.heads = hc;
   const int64_t grid = items * (p.Hkv / p.heads) + tiles;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  // block CTAs before CTA c: c * n / grid, rounded down (the share is rounded up
+  // by less than 2^-32, so the last one counts)
+  p.block_share = (((uint64_t)(grid - tiles) << 32) + (uint64_t)grid - 1) / (uint64_t)grid;
   if (p.bs == 64) {
     if (cache == SEER_CACHE_BF16) return launch_blocks<64, SEER_CACHE_BF16>(p, grid, stream);
     if (cache == SEER_CACHE_E4M3) return launch_blocks<64, SEER_CACHE_E4M3>(p, grid, stream);

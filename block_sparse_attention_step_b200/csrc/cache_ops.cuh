@@ -32,6 +32,7 @@ struct AppendParams {
   int segments, segment_rows;  // parts a token's rows are cut into, one warp each
   int items;        // touched blocks at most
   int heads;        // KV heads of a block per CTA (divides Hkv)
+  uint64_t block_share;  // 2^32 x block CTAs / all CTAs, rounded up
 };
 
 cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t stream);

@@ -540,9 +540,12 @@ def seer_rope_table(max_position: int, rotary_dim: int, base: float = 10000.0, t
                             device=device or torch.device("cuda", torch.cuda.current_device()))
     if tuple(table.shape) != (max_position, rotary_dim):
         raise ValueError("table must be [max_position][rotary_dim]")
+    at = _ptr(table, torch.float32, "table")
+    if table.device.index != torch.cuda.current_device():
+        raise ValueError(f"seer_rope_table: table on {table.device}, current device is "
+                         f"cuda:{torch.cuda.current_device()}")
     _check("seer_rope_table", _lib().seer_rope_table(
-        int(max_position), int(rotary_dim), float(base), _ptr(table, torch.float32, "table"),
-        _stream(stream)))
+        int(max_position), int(rotary_dim), float(base), at, _stream(stream)))
     return table
 
 

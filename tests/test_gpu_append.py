@@ -404,3 +404,18 @@ def test_empty_call_and_another_stream():
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         run_and_check(s)
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_device_than_the_current_one_are_refused(monkeypatch):
+    require_gpu()
+    s = setup_case(1, 2, 1, 64, [0], [3], seed=15)
+    a = seer.append_args(s["k"], s["v"], s["kp"], s["vp"], s["table"].cuda(), s["seqlens"], cu_tokens=s["cu"], max_new=3)
+    table = torch.full((8, 16), 7.0, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)         # no second one is needed: nothing is launched
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        seer.seer_append_rope(s["dims"], a)
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        seer.seer_rope_table(8, 16, table=table)
+    monkeypatch.undo()
+    assert (table == 7).all()
