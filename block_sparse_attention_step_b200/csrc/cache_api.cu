@@ -83,10 +83,24 @@ constexpr int kClusterMax = 8;  // CTAs that join one row's pieces without a par
 //   128 rows of 52 stages, e4m3     30.0 / 27.3 / 27.3 / 35.5 / 39.0   rule: 3
 //   256 rows of 58, e4m3            51.2 / 68.8 / 57.9 / 62.9          rule: 1
 //   512 rows of 58, e4m3           117.5 / 106.5 / 105.2 / 110.4       rule: 2
-//   512 ragged rows to 104, int8   118.7 / 110.9 / 112.7 / 116 / 155   rule: 2
+//   512 ragged rows to 104, int8   116.0 / 106.4 / 109.9 / 118         rule: 2
 //   512 ragged rows to 66, bf16      146 / 156 / 158 / 160 / 202       rule: 1
 //   1 row of 8, e4m3                 8.3 / 7.1 / 6.5 / 5.4 / 4.9       rule: 8
 constexpr int kPieceStart = 11, kCombineStages = 5;
+
+int ctas_per_sm(const seer_dims* d, int cache) {
+  return cache == SEER_CACHE_BF16 || d->num_q_heads / d->num_kv_heads > 8 ? 2 : 3;
+}
+
+// Whether the rows go out longest sequence first: where they do not all fit on
+// the SMs at once, so that the last to start are short (64 ragged sequences of 4K
+// to 32K x 8 heads, int8: 106 us, in the order they come 112).  Ranking costs a
+// CTA half a microsecond, which window rows, mostly as long as the window, do
+// not get back (147.5 against 146.9).
+bool longest_first(const seer_dims* d, int32_t splits, int per_sm) {
+  const int64_t ctas = (int64_t)d->batch * d->num_kv_heads * splits;
+  return d->batch > 1 && d->batch <= kRankedBatch && ctas > (int64_t)num_sms_current() * per_sm;
+}
 
 int32_t pick_splits(const seer_dims* d, int64_t stages, int ctas_per_sm) {
   const int64_t rows = (int64_t)d->batch * d->num_kv_heads;
@@ -176,6 +190,7 @@ seer_status cache_decode(const seer_dims* d, const seer_cache_attn_args* a, bool
   p.C = S < kClusterMax ? S : kClusterMax;
   p.num_pages = d->num_pages;
   p.scale_log2 = a->softmax_scale * kLog2e;
+  p.by_length = !window && longest_first(d, S, ctas_per_sm(d, a->cache_type));
   if (S > p.C) {
     const size_t parts = (size_t)d->batch * d->num_q_heads * (S / p.C);
     p.o_part = static_cast<float*>(a->workspace);
@@ -201,9 +216,8 @@ extern "C" {
 
 int32_t seer_sparse_decode_q8_splits(const seer_dims* d, int32_t k_max) {
   if (check_dims(d) != SEER_OK || k_max < 1) return 1;
-  // resident CTAs per SM: 3, or 2 with more than 8 heads to a group
-  const int per_sm = d->num_q_heads / d->num_kv_heads > 8 ? 2 : 3;
-  return pick_splits(d, (int64_t)k_max * (d->block_size / kTileTokens), per_sm);
+  return pick_splits(d, (int64_t)k_max * (d->block_size / kTileTokens),
+                     ctas_per_sm(d, SEER_CACHE_E4M3));
 }
 
 int32_t seer_window_decode_splits(const seer_dims* d, int32_t window, int32_t sinks) {

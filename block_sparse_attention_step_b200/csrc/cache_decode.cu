@@ -40,7 +40,7 @@
 // bf16, 64 sequences x 8 heads, window 4096: 146 us, 6.7 TB/s.  8 bit: 128-byte
 // rows 1 KB apart (token-major pages of 8 heads) are what bounds it; the copies
 // without the math take 25.3 of 27.3 us (16 x 32K tokens, 10 % of the blocks,
-// 109 MB) and 95.6 of 111 us (64 ragged sequences, 485 MB).  One row of 512
+// 109 MB) and 95.6 of 106 us (64 ragged sequences, 485 MB).  One row of 512
 // tokens takes 4.9 us in 8 pieces: launch, three dependent loads, a copy, the join.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -57,6 +57,7 @@ namespace seer {
 constexpr int kCDMath = 4;  // math warps
 constexpr int kCDThreads = (kCDMath + 1) * 32;
 constexpr int kCDCluster = 8;
+constexpr int kCDRanked = kRankedBatch;  // sequences ranked by length, at most
 constexpr float kCDSlack = 8.f;      // log2 of the largest P
 constexpr float kZeroScaleLog2 = -60.f;
 constexpr float kZeroScaleInv = 1.152921504606846976e18f;  // 2^60
@@ -177,12 +178,15 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
   __shared__ CDMeta meta[kStages];
   __shared__ float ml[kCDMath][2][kMaxGroup];  // per warp: M, l
   __shared__ float cta_ml[2][kMaxGroup];       // this CTA's M, l
+  __shared__ __align__(16) int lens[kCDRanked];  // p.by_length
+  __shared__ int ranked_b;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.G, S = p.S;
-  const int row = (int)(blockIdx.x / (unsigned)S);
+  const int place = (int)(blockIdx.x / (unsigned)S);  // of the row in the grid
   const int s = (int)(blockIdx.x % (unsigned)S);
-  const int b = row / p.Hkv, h = row - b * p.Hkv;
+  int b = place / p.Hkv;
+  const int h = place - b * p.Hkv;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -194,6 +198,25 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
+  if (!WINDOW && p.by_length) {
+    // the b-th longest sequence (of equal ones the first): every thread ranks its own
+    const int B4 = (p.B + 3) & ~3;
+    for (int i = threadIdx.x; i < B4; i += kCDThreads) lens[i] = i < p.B ? __ldg(p.seqlens + i) : INT_MIN;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.B; i += kCDThreads) {
+      const int mine = lens[i];
+      int rank = 0;
+      for (int j = 0; j < B4; j += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(lens + j);
+        rank += (o.x > mine || (o.x == mine && j < i)) + (o.y > mine || (o.y == mine && j + 1 < i)) +
+                (o.z > mine || (o.z == mine && j + 2 < i)) + (o.w > mine || (o.w == mine && j + 3 < i));
+      }
+      if (rank == b) ranked_b = i;
+    }
+    __syncthreads();
+    b = ranked_b;
+  }
+  const int row = b * p.Hkv + h;
   const CDRow rw = cd_row<WINDOW>(p, row, b);
   const int lo = (int)((long long)s * rw.nst / S);
   const int n = (int)((long long)(s + 1) * rw.nst / S) - lo;

@@ -39,6 +39,8 @@ cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t
 cudaError_t run_rope_table(float* table, int max_position, int rot, double base,
                            cudaStream_t stream);
 
+constexpr int kRankedBatch = 256;
+
 // Decode attention over a block list or a window with sinks.
 struct CacheDecodeParams {
   const uint16_t* q;  // [B][Hq][D]
@@ -56,6 +58,7 @@ struct CacheDecodeParams {
   int B, Hq, Hkv, G, bs, max_blocks, k_max, window, sinks;
   int S, C;         // pieces per row, CTAs per cluster (C = min(S, 8), divides S)
   int token_inner;  // tensor map dims are (D, token, head, page), not (D, head, token, page)
+  int by_length;    // longest sequences first (B <= kRankedBatch)
   int64_t num_pages;
   float scale_log2;
 };

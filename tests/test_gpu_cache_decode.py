@@ -361,3 +361,39 @@ def test_captured_graphs_with_their_own_workspaces_replay_together():
     torch.cuda.synchronize()
     for q, out, lse, graph, side in sides:
         check(c, q, seen, out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,G", [(40, 4), (41, 16), (256, 1), (300, 2)])
+def test_rows_of_large_ragged_batches_go_where_they_belong(B, G):
+    """More CTAs than fit at once go out longest sequence first (to 256 sequences): every row has the bits that it has in
+    a small batch.  Lengths repeat, and some are 0."""
+    require_gpu()
+    Hkv, bs, nbmax, S = 8, 64, 6, 2
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, nbmax * bs + 1, (B,), generator=g, dtype=torch.int32)
+    lens[::7] = 100
+    lens[3::11] = 0
+    pages = 64
+    k, v = [torch.randint(-127, 128, (pages, bs, Hkv, D), generator=g, dtype=torch.int8).cuda() for _ in range(2)]
+    ks, vs = [torch.rand((pages, Hkv), generator=g).cuda() * 0.02 + 0.001 for _ in range(2)]
+    table = torch.randint(0, pages, (B, nbmax), generator=g, dtype=torch.int32)
+    q = queries(B, Hkv * G, B)
+    idx = torch.arange(nbmax, dtype=torch.int32).repeat(B, Hkv, 1).cuda()
+    n_sel = ((lens + bs - 1) // bs)[:, None].repeat(1, Hkv).int()
+    n_sel[:, 1] = torch.clamp(n_sel[:, 1] - 1, min=0)
+    got = []
+    for step in (B, 9):
+        out, lse, status = torch.full_like(q, 7), torch.full((B, Hkv * G), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        for i in range(0, B, step):
+            n = min(step, B - i)
+            d = seer.make_dims(n, Hkv * G, Hkv, D, bs, nbmax, pages)
+            a = seer.sparse_decode_q8_args(q[i:i + n], k, v, table[i:i + n].cuda(), lens[i:i + n].cuda(), idx[i:i + n], n_sel[i:i + n].cuda(), k_scale=ks,
+                                           v_scale=vs, k_max=nbmax, num_splits=S, softmax_scale=SCALE, out=out[i:i + n], lse_out=lse[i:i + n], dev_status=status)
+            seer.seer_sparse_decode_q8(d, a)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    empty = (lens == 0).cuda()
+    assert (got[0][0][empty] == 0).all() and got[0][1][empty].isneginf().all() and got[0][0][~empty].abs().amax((1, 2)).min() > 0
