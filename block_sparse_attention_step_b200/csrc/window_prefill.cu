@@ -31,8 +31,8 @@
 // Where there are too few row tiles for the SMs (a short chunk behind a long
 // context) the CTAs of a cluster take a part of a tile's keys each and join their
 // states (O, maximum, sum in fp32) over distributed shared memory.  8K prompt (40/8 heads, window 2048, 301
-// GFLOP): 363 us in a loop at the power limit, 333 in a burst (903 TFLOP/s); ragged
-// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 98 to 104.  N 128 with two Q
+// GFLOP): 363 us in a loop at the power limit, 329 in a burst (915 TFLOP/s); ragged
+// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 98 to 107.  N 128 with two Q
 // tiles per CTA and one CTA per SM took 364 to 398, and 17 us instead of 10.7 on a
 // chunk of 77 tokens.
 #include <cooperative_groups.h>
@@ -241,7 +241,10 @@ __global__ void __launch_bounds__(kWPThreads, 2)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int piece = (int)blockIdx.x % C;
   const int h = (int)blockIdx.x / C % p.Hkv;
-  const int item = (int)blockIdx.x / C / p.Hkv;
+  // last row tiles first: a prompt's first ones see few keys, so the grid ends
+  // with short CTAs (full causal prompts of 2K / 4K tokens, 32/8 heads: 43 / 131 us
+  // instead of 53 / 149)
+  const int item = (int)((gridDim.x - 1 - blockIdx.x) / C) / p.Hkv;
 
   // ---- which sequence and which of its token tiles (warp 0); meanwhile
   // tensor memory (warp 1), barriers (warp 2), tensor maps (warp 3)
