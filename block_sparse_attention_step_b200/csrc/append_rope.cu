@@ -411,7 +411,7 @@ __device__ __forceinline__ Touched find_block(const AppendParams& p, int item) {
     return t;
   }
   const int lane = threadIdx.x & 31;
-  int passed = 0;  // touched blocks of the sequences before this round
+  int passed = 0;  // touched blocks of the sequences before these 32
   for (int base = 0; base < p.B && t.b < 0; base += 32) {
     const int b = base + lane;
     Seq s = {0, 0, 0};

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
       const int cnt = min(32, n - base);
       const int tok = page < 0 ? 1 << 28  // nothing of this stage is visible
                                : j * p.bs + (lo + base + lane) % nsub * kTileTokens;
-      auto issue = [&](int i) {  // stage i of this round
+      auto issue = [&](int i) {  // stage i of these 32
         const int k = base + i, slot = k % kStages;
         const int pg = max(0, __shfl_sync(0xffffffffu, page, i));
         const int sub = (lo + k) % nsub;

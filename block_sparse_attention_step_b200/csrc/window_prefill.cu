@@ -241,40 +241,48 @@ __global__ void __launch_bounds__(kWPThreads, 2)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int piece = (int)blockIdx.x % C;
   const int h = (int)blockIdx.x / C % p.Hkv;
-  // last row tiles first: a prompt's first ones see few keys, so the grid ends
-  // with short CTAs (full causal prompts of 2K / 4K tokens, 32/8 heads: 43 / 131 us
-  // instead of 53 / 149)
-  const int item = (int)((gridDim.x - 1 - blockIdx.x) / C) / p.Hkv;
+  int item = (int)blockIdx.x / C / p.Hkv;
 
   // ---- which sequence and which of its token tiles (warp 0); meanwhile
   // tensor memory (warp 1), barriers (warp 2), tensor maps (warp 3)
   pdl_launch_dependents();
   if (warp == 0) {
     pdl_wait();  // every other read of global memory comes after the barrier below
-    int passed = 0, found_b = -1, found_tile = 0;
+    // Row tiles that see a whole window first (whatever their order), then those
+    // near the start of their sequence, the longest of each first, so that the
+    // grid ends with short CTAs (full causal prompts of 2K / 4K tokens, 32/8 heads:
+    // 43 / 131 us, in the order of the rows 53 / 149).
+    int found_b = -1, found_tile = 0;
     Seq found = {0, 0, 0};
-    for (int base = 0; base < p.B && found_b < 0; base += 32) {
-      const int b = base + lane;
-      Seq s = {0, 0, 0};
-      if (b < p.B) s = load_seq(p.cu, p.seqlens, b, p.T, p.max_new, p.max_blocks * p.bs, p.status);
-      const int cnt = ceil_div_i(s.n, p.ntok);
-      int incl = cnt;
+    for (int near = 0; near < 2 && found_b < 0; ++near) {
+      int passed = 0;
+      for (int base = 0; base < p.B && found_b < 0; base += 32) {
+        const int b = base + lane;
+        Seq s = {0, 0, 0};
+        if (b < p.B) s = load_seq(p.cu, p.seqlens, b, p.T, p.max_new, p.max_blocks * p.bs, p.status);
+        const int all = ceil_div_i(s.n, p.ntok);
+        const int at_start = min(all, ceil_div_i(max(0, p.window - (s.L - s.n)), p.ntok));
+        const int cnt = near ? at_start : all - at_start;
+        int incl = cnt;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const int lo = passed + incl - cnt;
+        const unsigned hit = __ballot_sync(0xffffffffu, item >= lo && item < lo + cnt);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          found_b = base + src;
+          found_tile = __shfl_sync(
+              0xffffffffu, near ? at_start - 1 - (item - lo) : at_start + (item - lo), src);
+          found.first = __shfl_sync(0xffffffffu, s.first, src);
+          found.n = __shfl_sync(0xffffffffu, s.n, src);
+          found.L = __shfl_sync(0xffffffffu, s.L, src);
+        }
+        passed += __shfl_sync(0xffffffffu, incl, 31);
       }
-      const int lo = passed + incl - cnt;
-      const unsigned hit = __ballot_sync(0xffffffffu, item >= lo && item < lo + cnt);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        found_b = base + src;
-        found_tile = item - __shfl_sync(0xffffffffu, lo, src);
-        found.first = __shfl_sync(0xffffffffu, s.first, src);
-        found.n = __shfl_sync(0xffffffffu, s.n, src);
-        found.L = __shfl_sync(0xffffffffu, s.L, src);
-      }
-      passed += __shfl_sync(0xffffffffu, incl, 31);
+      item -= passed;
     }
     if (lane == 0) {
       bars.b = found_b;
