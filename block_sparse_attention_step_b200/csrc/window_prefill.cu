@@ -32,7 +32,7 @@
 // context) the CTAs of a cluster take a part of a tile's keys each and join their
 // states (O, maximum, sum in fp32) over distributed shared memory.  8K prompt (40/8 heads, window 2048, 301
 // GFLOP): 363 us in a loop at the power limit, 329 in a burst (915 TFLOP/s); ragged
-// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 98 to 107.  N 128 with two Q
+// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 91 to 97.  N 128 with two Q
 // tiles per CTA and one CTA per SM took 364 to 398, and 17 us instead of 10.7 on a
 // chunk of 77 tokens.
 #include <cooperative_groups.h>
@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kWPThreads, 2)
     // Row tiles that see a whole window first (whatever their order), then those
     // near the start of their sequence, the longest of each first, so that the
     // grid ends with short CTAs (full causal prompts of 2K / 4K tokens, 32/8 heads:
-    // 43 / 131 us, in the order of the rows 53 / 149).
+    // 45 / 136 us, in the order of the rows 53 / 149; ragged chunks 91, the other
+    // way round 97 to 104).
     int found_b = -1, found_tile = 0;
     Seq found = {0, 0, 0};
     for (int near = 0; near < 2 && found_b < 0; ++near) {
