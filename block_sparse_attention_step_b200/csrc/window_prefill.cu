@@ -32,7 +32,7 @@
 // context) the CTAs of a cluster take a part of a tile's keys each and join their
 // states (O, maximum, sum in fp32) over distributed shared memory.  8K prompt (40/8 heads, window 2048, 301
 // GFLOP): 363 us in a loop at the power limit, 329 in a burst (915 TFLOP/s); ragged
-// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 91 to 97.  N 128 with two Q
+// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 91 to 102.  N 128 with two Q
 // tiles per CTA and one CTA per SM took 364 to 398, and 17 us instead of 10.7 on a
 // chunk of 77 tokens.
 #include <cooperative_groups.h>
@@ -255,7 +255,11 @@ __global__ void __launch_bounds__(kWPThreads, 2)
     // way round 97 to 104).
     int found_b = -1, found_tile = 0;
     Seq found = {0, 0, 0};
-    for (int near = 0; near < 2 && found_b < 0; ++near) {
+    if (p.max_new == 1 && item < p.B) {  // a row tile per sequence
+      found = load_seq(p.cu, p.seqlens, item, p.T, 1, p.max_blocks * p.bs, p.status);
+      if (found.n > 0) found_b = item;
+    }
+    for (int near = p.max_new == 1 ? 2 : 0; near < 2 && found_b < 0; ++near) {
       int passed = 0;
       for (int base = 0; base < p.B && found_b < 0; base += 32) {
         const int b = base + lane;

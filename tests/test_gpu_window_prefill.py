@@ -369,3 +369,42 @@ def test_prompt_chunk_and_decode_over_one_cache():
                     tol = 2 * 2.0 ** -8 * size * np.abs(V[seen][:, h]).max() + 2 * 2.0 ** -8 * np.abs(V[seen][:, h]).max()
                     assert np.abs(got[t, qh] - want).max() <= tol
                     assert np.linalg.norm(got[t, qh] - want) <= 1e-2 * np.linalg.norm(want) + 2.0 ** -8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("with_cu", [True, False])
+def test_a_token_for_each_of_many_sequences(with_cu):
+    """Many single tokens, some sequences without one, one too long: the others agree with a call of their own."""
+    require_gpu()
+    B, Hkv, G, bs, nbmax, pages = 150, 2, 4, 64, 5, 40
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(1, nbmax * bs + 1, (B,), generator=g, dtype=torch.int32)
+    new = torch.ones(B, dtype=torch.int32)
+    new[5::9] = 0
+    lens[5::9] = 0
+    lens[20] = nbmax * bs + 1
+    if not with_cu:
+        new[:] = 1
+    cu = torch.cat([torch.zeros(1), new.cumsum(0)]).int()
+    T = int(cu[-1])
+    k, v = [torch.randn((pages, bs, Hkv, D), generator=g).bfloat16().cuda() for _ in range(2)]
+    table = torch.randint(0, pages, (B, nbmax), generator=g, dtype=torch.int32)
+    q = torch.randn((T, Hkv * G, D), generator=g).bfloat16().cuda()
+    out, lse, status = torch.full_like(q, 7), torch.full((Hkv * G, T), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    d = seer.make_dims(B, Hkv * G, Hkv, D, bs, nbmax, pages)
+    seer.seer_window_prefill(d, seer.window_prefill_args(q, k, v, table.cuda(), lens.cuda(), cu_tokens=cu.cuda() if with_cu else None, max_new=1, window=90, sinks=3,
+                                                         softmax_scale=SCALE, out=out, lse_out=lse, dev_status=status))
+    assert status.item() == seer.DEV_BAD_TOKENS
+    for b in range(B):
+        row = int(cu[b])
+        if new[b] == 0:
+            continue
+        if lens[b] in (0, nbmax * bs + 1):
+            assert (out[row] == 7).all() and (lse[:, row] == 7).all()
+            continue
+        o, l = torch.full_like(q[:1], 7), torch.full((Hkv * G, 1), 7.0, device="cuda")
+        d1 = seer.make_dims(1, Hkv * G, Hkv, D, bs, nbmax, pages)
+        seer.seer_window_prefill(d1, seer.window_prefill_args(q[row:row + 1], k, v, table[b:b + 1].cuda(), lens[b:b + 1].cuda(), window=90, sinks=3, softmax_scale=SCALE,
+                                                              out=o, lse_out=l))
+        # keys split over another number of CTAs: both round their weights and outputs to bf16
+        assert (o[0].float() - out[row].float()).abs().max() <= 4 * 2.0 ** -8 * v.float().abs().max() and (l[:, 0] - lse[:, row]).abs().max() <= 1e-4
