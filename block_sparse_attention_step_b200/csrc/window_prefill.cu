@@ -57,10 +57,6 @@ constexpr size_t kWPData = 2 * kWPHalf + (size_t)(kWPKStages + kWPVStages) * kWP
 constexpr int kWPCluster = 8;                 // pieces of a tile's keys, at most
 constexpr size_t kWPSmem = kWPData + 1024;    // alignment slack, which holds the barriers too
 constexpr float kWPSlack = 8.f;
-// One pair in so many takes its 2^y from the FMA pipe.  8K prompt (40/8 heads,
-// window 2048, at the power limit): every 4th 376 us, every 8th 369, none 365;
-// ragged chunks: 98 / 101 / 102 (the exponentials bound neither).
-constexpr int kWPPolyEvery = 8;
 constexpr uint32_t kWPIdescS = tc_idesc_bf16(kWPRows, kWPKeys, 0, 0);
 constexpr uint32_t kWPIdescPV = tc_idesc_bf16(kWPRows, kHeadDim, 0, 1);
 constexpr uint32_t kWPCols = 256;             // TMEM: S 2 x 64, O 128
@@ -99,29 +95,6 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)),
       "l"(policy)
       : "memory");
-}
-
-// 2^y of a pair, y <= 8, on the FMA pipe: y = n + f with n its nearest integer,
-// 2^f by the degree-5 polynomial of least relative error on [-1/2, 1/2] (Remez
-// exchange; 2.3e-7 in fp32), times 2^n.  y below -126 gives 2^-126, NaN gives
-// NaN.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t y2) {
-  float a, b;
-  unpack2(y2, a, b);
-  y2 = pack2(max_nan(a, -126.f), max_nan(b, -126.f));
-  const uint64_t magic = pack2(12582912.f, 12582912.f), unmagic = pack2(-12582912.f, -12582912.f);
-  const uint64_t t2 = add2(y2, magic);
-  const uint64_t f2 = fma2(add2(t2, unmagic), pack2(-1.f, -1.f), y2);
-  uint64_t r = pack2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
-  r = fma2(r, f2, pack2(9.675540961325169e-3f, 9.675540961325169e-3f));
-  r = fma2(r, f2, pack2(5.550713092088699e-2f, 5.550713092088699e-2f));
-  r = fma2(r, f2, pack2(2.4022120237350464e-1f, 2.4022120237350464e-1f));
-  r = fma2(r, f2, pack2(6.931469440460205e-1f, 6.931469440460205e-1f));
-  r = fma2(r, f2, pack2(1.0000001192092896f, 1.0000001192092896f));
-  float ta, tb;
-  unpack2(t2, ta, tb);
-  return mul2(r, pack2(__uint_as_float((__float_as_uint(ta) << 23) + 0x3f800000u),
-                       __uint_as_float((__float_as_uint(tb) << 23) + 0x3f800000u)));
 }
 
 // The lowest n of 64 bits (n clamped to 0 .. 64).
@@ -570,17 +543,11 @@ __global__ void __launch_bounds__(kWPThreads, 2)
       for (int c = 0; c < 32; ++c) {
         const uint64_t y2 = fma2(pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])),
                                  scale2, ref2);
-        uint64_t e2;
-        if (c % kWPPolyEvery == kWPPolyEvery - 1) {
-          e2 = exp2_poly2(y2);
-        } else {
-          float a, e;
-          unpack2(y2, a, e);
-          e2 = pack2(fast_exp2(a), fast_exp2(e));
-        }
-        sum2[c & 1] = add2(sum2[c & 1], e2);
         float a, e;
-        unpack2(e2, a, e);
+        unpack2(y2, a, e);
+        a = fast_exp2(a);  // exp2(-inf) = 0: a key that the row does not see weighs nothing
+        e = fast_exp2(e);
+        sum2[c & 1] = add2(sum2[c & 1], pack2(a, e));
         pk[c] = pack_bf16x2(a, e);
       }
       __syncwarp();

@@ -408,3 +408,37 @@ def test_a_token_for_each_of_many_sequences(with_cu):
                                                               out=o, lse_out=l))
         # keys split over another number of CTAs: both round their weights and outputs to bf16
         assert (o[0].float() - out[row].float()).abs().max() <= 4 * 2.0 ** -8 * v.float().abs().max() and (l[:, 0] - lse[:, row]).abs().max() <= 1e-4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hkv", [1, 100])
+@pytest.mark.parametrize("window,sinks,bs", [(70, 3, 64), (9, 0, 128), (400, 130, 64)])
+def test_large_values_that_a_query_does_not_see_weigh_nothing(window, sinks, bs, Hkv):
+    """Finite values next to bf16's largest, one dim of each token: where a query sees none of them in a dim, the dim is
+    as if they were not there, whatever the key's place in a tile.  One CTA for each row tile, and keys split over a cluster."""
+    require_gpu()
+    past, new, L = 200, 90, 290
+    c = make_cache([L], Hkv, bs, "bf16", seed=window)
+    t = np.arange(L)
+    pages = c["table"][0].numpy()[t // bs]
+    huge = np.zeros((L, D), dtype=bool)
+    for lo, first in ((past, 0), (max(0, past - window + 1), 32)):    # ahead of some queries, behind the window of some
+        for i in range(min(new, 96)):
+            huge[lo + i, first + i % 96] = True
+            c["v"][pages[lo + i], (lo + i) % bs, :, first + i % 96] = 3e38 if i % 2 else -3e38
+    G = 5
+    q, out, lse, _ = run(c, [past], [new], G * Hkv, window, sinks, seed=window)
+    K, V = values(c, "k"), values(c, "v")
+    qd, got = q.double().cpu().numpy(), out.double().cpu().numpy()
+    for h in {0, Hkv // 2, Hkv - 1}:
+        k, v = K[pages, t % bs, h], V[pages, t % bs, h]
+        for i in range(new):
+            seen = C.window_seen(past + i, L, window, sinks)
+            clean = ~huge[seen].any(0)
+            assert clean.any()
+            for qh in range(h * G, (h + 1) * G):
+                want, want_lse = C.softmax_attention(qd[i, qh], k, v[:, clean], seen, SCALE)
+                w = np.exp(k[seen] @ qd[i, qh] * SCALE - want_lse)
+                # weights and out rounded to bf16 (2^-8 each); 1e-4 for scores of this size
+                tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 1e-4) * (w @ np.abs(v[seen][:, clean]) + np.abs(want))
+                assert (np.abs(got[i, qh, clean] - want) <= tol).all(), (i, qh, np.abs(got[i, qh, clean] - want).max())
