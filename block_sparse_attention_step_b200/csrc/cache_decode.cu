@@ -8,7 +8,7 @@
 // pieces; up to 8 pieces are the CTAs of one thread-block cluster, which join
 // their softmax states over distributed shared memory and write out and lse
 // themselves.  Past 8 pieces each cluster writes one partial and the
-// log-sum-exp combine follows.  The order of every sum is fixed by the
+// log-sum-exp combine follows (whose fp32 weights end at 2^-126).  The order of every sum is fixed by the
 // shapes, so results do not change from run to run.
 //
 // A CTA is four math warps and a copy warp.  The copy warp resolves the
@@ -26,22 +26,24 @@
 // scaled per head by a power of two that puts its largest element near 2^14
 // (a bf16 value then fits f16 exactly unless it is 2^-28 of the largest).
 // A block's K scale multiplies its scores.  Its V scale enters the exponent:
-// with y_t = log2 w_t + log2 vs and a running reference M,
-//   O = sum 2^(y_t - M) code_t,   l = sum 2^(y_t - M) / vs,   out = O / l,
-// so a weight is rounded (to f16, 2^-11) relative to the largest contribution
-// to O, however far the blocks' scales lie apart.  A scale of 0 (all rows zero)
-// counts as 2^-60 with the codes taken as zero, which leaves l and O in range for
-// scales of 2^-70 to 2^40 beside it.
-// For a bf16 cache P enters as a bf16 hi + lo pair (2^-17).
+// with x_t = log2 w_t, y_t = x_t + log2 vs and a running reference for each,
+//   l = sum 2^(x_t - m),   O = sum 2^(y_t - M) code_t,   out = O / l * 2^(M - m),
+// so a weight in O is rounded (to f16, 2^-11) relative to the largest contribution
+// to O, and l loses nothing, however far the blocks' scales lie apart.  A block of
+// scale 0 (all rows zero) has y = -inf: it adds to l alone, its codes are
+// taken as zero.
+// For a bf16 cache y = x, and P enters as a bf16 hi + lo pair (2^-17).
 //
-// M moves only when a score exceeds it by more than 2^8 (P then stays below
-// 256): a vote per tile instead of a maximum over the warp, and no rescaling
-// of O in between.  Bound by HBM: 256 B (bf16: 512) per token and KV head.
+// A reference moves only when a score exceeds it by more than 2^8 (P then stays
+// below 256): a vote per tile instead of a maximum over the warp, and no
+// rescaling of O or l in between.  Bound by HBM: 256 B (bf16: 512) per token and KV head.
 // bf16, 64 sequences x 8 heads, window 4096: 146 us, 6.7 TB/s.  8 bit: 128-byte
 // rows 1 KB apart (token-major pages of 8 heads) are what bounds it; the copies
-// without the math take 25.3 of 27.3 us (16 x 32K tokens, 10 % of the blocks,
-// 109 MB) and 95.6 of 106 us (64 ragged sequences, 485 MB).  One row of 512
-// tokens takes 4.9 us in 8 pieces: launch, three dependent loads, a copy, the join.
+// without the math take 25.3 of 28.4 us (16 x 32K tokens, 10 % of the blocks,
+// 109 MB) and 95.6 of 108 us (64 ragged sequences, 485 MB).  The second reference
+// and exponential of a token, without which l lost tokens whose V scale is 2^100
+// below another's, are 0.8 and 1.5 us of these.  One row of 512 tokens takes
+// 5.1 us in 8 pieces: launch, three dependent loads, a copy, the join.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -59,8 +61,6 @@ constexpr int kCDThreads = (kCDMath + 1) * 32;
 constexpr int kCDCluster = 8;
 constexpr int kCDRanked = kRankedBatch;  // sequences ranked by length, at most
 constexpr float kCDSlack = 8.f;      // log2 of the largest P
-constexpr float kZeroScaleLog2 = -60.f;
-constexpr float kZeroScaleInv = 1.152921504606846976e18f;  // 2^60
 
 template <int CACHE>
 struct CDShape {
@@ -74,9 +74,9 @@ struct CDShape {
 };
 
 struct __align__(16) CDMeta {
-  int base;           // position of the stage's token 0
-  float ks;           // K scale
-  float lv, inv;      // log2 and inverse of the V scale
+  int base;  // position of the stage's token 0
+  float ks;  // K scale
+  float lv;  // log2 of the V scale, -inf: 0
 };
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
                                              ~uintptr_t(1023));
   __shared__ uint64_t full_bar[kStages], empty_bar[kStages];
   __shared__ CDMeta meta[kStages];
-  __shared__ float ml[kCDMath][2][kMaxGroup];  // per warp: M, l
-  __shared__ float cta_ml[2][kMaxGroup];       // this CTA's M, l
+  __shared__ float ml[kCDMath][3][kMaxGroup];  // per warp: M, m, l
+  __shared__ float cta_ml[3][kMaxGroup];       // this CTA's M, m, l
   __shared__ __align__(16) int lens[kCDRanked];  // p.by_length
   __shared__ int ranked_b;
 
@@ -222,10 +222,10 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
   const int n = (int)((long long)(s + 1) * rw.nst / S) - lo;
   const int C = p.C;
 
-  float m[NT][2], l[NT][2], o[8][NT][4];
+  float m[NT][2], my[NT][2], l[NT][2], o[8][NT][4];  // references of l (m) and, 8-bit cache, of O (my)
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY;
+    m[nt][0] = m[nt][1] = my[nt][0] = my[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
@@ -299,12 +299,7 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
         vs = scale_at(p.v_scale, page);
         for (; issued < min(cnt, kStages); ++issued) issue(issued);
       }
-      float lv = 0.f, inv = 1.f;
-      if constexpr (!kBf16) {
-        // negative inverse: the scale is zero and the codes count as zero
-        lv = vs == 0.f ? kZeroScaleLog2 : log2f(vs);
-        inv = vs == 0.f ? -kZeroScaleInv : 1.f / vs;
-      }
+      const float lv = kBf16 ? 0.f : log2f(vs);
       for (int i = 0; i < cnt; ++i) {
         const int k = base + i, slot = k % kStages;
         if (i >= issued) {
@@ -320,7 +315,6 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
         mt.base = __shfl_sync(0xffffffffu, tok, i);
         mt.ks = __shfl_sync(0xffffffffu, ks, i);
         mt.lv = __shfl_sync(0xffffffffu, lv, i);
-        mt.inv = __shfl_sync(0xffffffffu, inv, i);
         if (lane == 0) {
           meta[slot] = mt;
           mbar_arrive(&full_bar[slot]);
@@ -488,47 +482,59 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
           if (!v3) vw[3] = z;
         }
       }
-      float inv = mt4.inv;
       if constexpr (!kBf16) {
-        if (inv < 0.f) {
-          inv = -inv;
+        if (mt4.lv == -INFINITY) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) vw[i] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
 
-      // ---- weights relative to the lazily moved reference
+      // ---- weights relative to the lazily moved references
       float x[NT][4];
       bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
+        // a score past this moves a reference (-inf less -inf, a NaN, leaves m's)
+        float top[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          top[e] = (kBf16 ? m[nt][e] : fminf(m[nt][e], my[nt][e] - mt4.lv)) + kCDSlack;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = sacc[nt][0][e] + sacc[nt][1][e];
           const bool in = e < 2 ? in0 : in1;
-          if constexpr (kBf16) x[nt][e] = in ? v * cs[nt][e & 1] : -INFINITY;
-          else x[nt][e] = in ? fmaf(v, cs[nt][e & 1] * mt4.ks, mt4.lv) : -INFINITY;
-          over |= x[nt][e] > m[nt][e & 1] + kCDSlack;
+          x[nt][e] = in ? v * (kBf16 ? cs[nt][e & 1] : cs[nt][e & 1] * mt4.ks) : -INFINITY;
+          over |= x[nt][e] > top[e & 1];
         }
       }
+      // the factor by which what was summed shrinks when a reference moves to
+      // the tile's maximum (over the warp's tokens of a head column)
+      auto move_to = [](float& ref, float a, float b) {
+        float mx = fmaxf(a, b);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float to = fmaxf(ref, mx);
+        const float alpha = to == -INFINITY ? 1.f : fast_exp2(ref - to);
+        ref = to;
+        return alpha;
+      };
+      auto shrink_o = [&](int nt, int e, float alpha) {
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          o[mt][nt][e] *= alpha;
+          o[mt][nt][2 + e] *= alpha;
+        }
+      };
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(x[nt][e], x[nt][2 + e]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m[nt][e], mx);
-            const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m[nt][e] - mn);
-            m[nt][e] = mn;
+            const float alpha = move_to(m[nt][e], x[nt][e], x[nt][2 + e]);
             l[nt][e] *= alpha;
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt) {
-              o[mt][nt][e] *= alpha;
-              o[mt][nt][2 + e] *= alpha;
-            }
+            if constexpr (kBf16) shrink_o(nt, e, alpha);
+            else shrink_o(nt, e, move_to(my[nt][e], x[nt][e] + mt4.lv, x[nt][2 + e] + mt4.lv));
           }
         }
       }
@@ -541,9 +547,9 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
           const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
           pr[e] = fast_exp2(x[nt][e] - ref);
         }
+        l[nt][0] += pr[0] + pr[2];
+        l[nt][1] += pr[1] + pr[3];
         if constexpr (kBf16) {
-          l[nt][0] += pr[0] + pr[2];
-          l[nt][1] += pr[1] + pr[3];
           uint32_t h0, l0, h1, l1;
           split_bf16x2(pr[0], pr[1], h0, l0);
           split_bf16x2(pr[2], pr[3], h1, l1);
@@ -552,8 +558,11 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
           pl[nt][0] = movmatrix_trans(l0);
           pl[nt][1] = movmatrix_trans(l1);
         } else {
-          l[nt][0] = fmaf(pr[0] + pr[2], inv, l[nt][0]);
-          l[nt][1] = fmaf(pr[1] + pr[3], inv, l[nt][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ref = my[nt][e & 1] == -INFINITY ? 0.f : my[nt][e & 1];
+            pr[e] = fast_exp2(x[nt][e] + (mt4.lv - ref));
+          }
           ph[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
           ph[nt][1] = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
         }
@@ -622,8 +631,9 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
         const int g = nt * 8 + 2 * c + e;
         if (g < G) {
           if (r == 0) {
-            ml[warp][0][g] = m[nt][e];
-            ml[warp][1][g] = l[nt][e];
+            ml[warp][0][g] = kBf16 ? m[nt][e] : my[nt][e];
+            ml[warp][1][g] = m[nt][e];
+            ml[warp][2][g] = l[nt][e];
           }
           float* dst = ow + (size_t)(warp * G + g) * kHeadDim;
 #pragma unroll
@@ -644,21 +654,24 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
   float* co = ow + (size_t)kCDMath * G * kHeadDim;  // the CTA's state [head][dim]
   for (int e = threadIdx.x; e < G * kHeadDim; e += kCDThreads) {
     const int g = e / kHeadDim;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kCDMath; ++w) M = fmaxf(M, ml[w][0][g]);
-    float L = 0.f, O = 0.f;
-    const float ref = M == -INFINITY ? 0.f : M;
+    float M = -INFINITY, m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kCDMath; ++w) {
-      const float f = fast_exp2(ml[w][0][g] - ref);
-      L = fmaf(ml[w][1][g], f, L);
-      O = fmaf(ow[(size_t)w * G * kHeadDim + e], f, O);
+      M = fmaxf(M, ml[w][0][g]);
+      m = fmaxf(m, ml[w][1][g]);
+    }
+    float L = 0.f, O = 0.f;
+    const float ref_o = M == -INFINITY ? 0.f : M, ref_l = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < kCDMath; ++w) {
+      O = fmaf(ow[(size_t)w * G * kHeadDim + e], fast_exp2(ml[w][0][g] - ref_o), O);
+      L = fmaf(ml[w][2][g], fast_exp2(ml[w][1][g] - ref_l), L);
     }
     co[e] = O;
     if (e % kHeadDim == 0) {
       cta_ml[0][g] = M;
-      cta_ml[1][g] = L;
+      cta_ml[1][g] = m;
+      cta_ml[2][g] = L;
     }
   }
   // ---- join the cluster's CTAs: each takes its part of the outputs
@@ -668,26 +681,34 @@ __global__ void __launch_bounds__(kCDThreads, NT == 1 ? CDShape<CACHE>::kCtas : 
   const int rank = C > 1 ? (int)cluster.block_rank() : 0;
   for (int e = rank * kCDThreads + threadIdx.x; e < G * kHeadDim; e += C * kCDThreads) {
     const int g = e / kHeadDim, d = e - g * kHeadDim;
-    float Ms[kCDCluster], M = -INFINITY;
+    float Mq[kCDCluster], mq[kCDCluster], M = -INFINITY, m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kCDCluster; ++q) {
       if (q < C) {
-        Ms[q] = C > 1 ? *cluster.map_shared_rank(&cta_ml[0][g], q) : cta_ml[0][g];
-        M = fmaxf(M, Ms[q]);
+        Mq[q] = C > 1 ? *cluster.map_shared_rank(&cta_ml[0][g], q) : cta_ml[0][g];
+        mq[q] = kBf16 ? Mq[q] : C > 1 ? *cluster.map_shared_rank(&cta_ml[1][g], q) : cta_ml[1][g];
+        M = fmaxf(M, Mq[q]);
+        m = fmaxf(m, mq[q]);
       }
     }
-    const float ref = M == -INFINITY ? 0.f : M;
+    const float ref_o = M == -INFINITY ? 0.f : M, ref_l = m == -INFINITY ? 0.f : m;
     float L = 0.f, O = 0.f;
 #pragma unroll
     for (int q = 0; q < kCDCluster; ++q) {
       if (q < C) {
-        const float f = fast_exp2(Ms[q] - ref);
-        L = fmaf(C > 1 ? *cluster.map_shared_rank(&cta_ml[1][g], q) : cta_ml[1][g], f, L);
-        O = fmaf(C > 1 ? *cluster.map_shared_rank(&co[e], q) : co[e], f, O);
+        L = fmaf(C > 1 ? *cluster.map_shared_rank(&cta_ml[2][g], q) : cta_ml[2][g],
+                 fast_exp2(mq[q] - ref_l), L);
+        O = fmaf(C > 1 ? *cluster.map_shared_rank(&co[e], q) : co[e], fast_exp2(Mq[q] - ref_o), O);
       }
     }
-    const float v = L == 0.f ? 0.f : O / L;
-    const float lse = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    float v = L == 0.f ? 0.f : O / L;
+    if constexpr (!kBf16) {
+      // times 2^(M - m) by halves: the whole may lie below the normal numbers where
+      // its product with O / l does not
+      const float half = L == 0.f ? 0.f : fast_exp2(0.5f * (M - m));
+      v = v * half * half;
+    }
+    const float lse = L == 0.f ? -INFINITY : (m + log2f(L)) * kLn2;
     const int64_t orow = (int64_t)b * p.Hq + (int64_t)h * G + g;
     if (p.o_part != nullptr) {
       const int64_t part = orow * (S / C) + s / C;

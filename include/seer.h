@@ -483,8 +483,7 @@ SEER_API seer_status seer_step_workspace_init(const seer_dims *d, int32_t k_max,
  * layouts of a bf16 pool with one byte per element (strides in elements, all
  * multiples of 16) and two fp32 arrays k_scale, v_scale [num_pages][Hkv]: an
  * element is code * scale of its page and KV head.  A scale is 0, which says
- * that the page's rows of that head are all zero, or a number from 2^-70 to
- * 2^40 (the decodes take weights and V scales as one fp32 product). */
+ * that the page's rows of that head are all zero, or a positive finite number. */
 #define SEER_CACHE_BF16 0
 #define SEER_CACHE_E4M3 1 /* 8-bit float, 4 exponent and 3 mantissa bits, +-448 */
 #define SEER_CACHE_INT8 2 /* two's complement, -127 .. 127 */

@@ -397,3 +397,82 @@ def test_rows_of_large_ragged_batches_go_where_they_belong(B, G):
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     empty = (lens == 0).cuda()
     assert (got[0][0][empty] == 0).all() and got[0][1][empty].isneginf().all() and got[0][0][~empty].abs().amax((1, 2)).min() > 0
+
+
+def block_scales(c, exponents):
+    """Sets V's scales of sequence 0's blocks to 2^e (e None: 0, whose codes count as zero)."""
+    for j, e in enumerate(exponents):
+        page = c["table"][0, j]
+        c["vs"][page] = 0.0 if e is None else 2.0 ** e
+
+
+def check_far(c, q, seen, out, lse, splits, softmax_scale=SCALE):
+    """check() where single tokens or blocks take nearly all the weight.  A weight's f16 rounding is relative to the
+    largest of w_t vs_t (the running reference is at most that), so below 2^-14 of it a step is 2^-24: 2^-25 of it
+    times every token's code is added.  So is 2^-134, half the least step of bf16 numbers.  More than 8 pieces are joined
+    with the weights e^(lse_piece - the largest) in fp32, where those below 2^-126 are 0: a piece's out, at most the
+    largest value, may go missing with that weight.  Past bf16's largest number, 255 * 2^120, out is an infinity."""
+    K, V = values(c, "k"), values(c, "v")
+    qd, got, gl = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    G, vs = q.shape[1] // c["Hkv"], c["vs"].double().numpy()
+    for b in range(q.shape[0]):
+        t = np.arange(c["lens"][b])
+        pages = c["table"][b].numpy()[t // c["bs"]]
+        for h in range(c["Hkv"]):
+            s = seen[b][h]
+            k, v, scale = K[pages, t % c["bs"], h][s], V[pages, t % c["bs"], h][s], vs[pages, h][s]
+            codes = np.abs(v / np.where(scale > 0, scale, 1.0)[:, None]).sum(0)
+            for i in range(h * G, (h + 1) * G):
+                want, want_lse = C.softmax_attention(qd[b, i], k, v, np.ones(len(k), dtype=bool), softmax_scale)
+                size = (np.abs(k) @ np.abs(qd[b, i])).max() * abs(softmax_scale)
+                dx = 128 * 2.0 ** -24 * size + 2.0 ** -21
+                w = np.exp((k @ qd[b, i]) * softmax_scale - want_lse)
+                tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * dx) * (w @ np.abs(v) + np.abs(want)) + 2.0 ** -25 * (w * scale).max() * codes + 2.0 ** -134
+                tol += 2.0 ** -126 * np.abs(v).max() if splits > 8 else 0.0
+                past = (np.abs(want) + tol > 255 * 2.0 ** 120) & (got[b, i] == np.copysign(np.inf, want))
+                assert ((np.abs(got[b, i] - want) <= tol) | past).all(), (b, i, np.abs(got[b, i] - want).max(), tol.min())
+                assert abs(gl[b, i] - want_lse) <= 2 * dx + 4 * 2.0 ** -24 * abs(want_lse), (b, i, gl[b, i], want_lse)
+
+
+FAR = [[-118], [110], [-126, -100, -126], [-120, 0, 90, None, -60], [0, -119, 3, -108], [None, -126], [121, -126, 40, -70, None, 0]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["list", "window"])
+@pytest.mark.parametrize("cache,splits", [("e4m3", 1), ("int8", 3), ("e4m3", 8), ("int8", 16)])
+@pytest.mark.parametrize("far", range(len(FAR)))
+def test_value_scales_over_the_whole_range(far, cache, splits, form):
+    """V scales from the least normal number to the largest that rows can ask for, alone and side by side: out and lse
+    are those of the values, also where a block of tiny values takes all the weight."""
+    require_gpu()
+    L = 64 * 12 - 9
+    c = make_cache([L], 2, 64, cache, seed=far)
+    block_scales(c, [FAR[far][j % len(FAR[far])] for j in range(12)])
+    for heavy in (False, True):
+        if heavy:                                        # the first block's keys: some 40 above the others
+            page = c["table"][0, 0]
+            c["ks"][page] *= 4
+        q = queries(1, 12, far, 12.0 if heavy else 1.0)
+        seen = [[np.ones(L, dtype=bool)] * 2]
+        out, lse = run_list(c, q, [[list(range(12))] * 2], splits) if form == "list" else run_window(c, q, L, 0, splits)[:2]
+        check_far(c, q, seen, out, lse, splits)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+@pytest.mark.parametrize("splits", [1, 4, 16])
+def test_zero_block_that_takes_all_the_weight(cache, splits):
+    """A block of zero values whose scores lie 60 above the others': out is the others' share, as small as it is."""
+    require_gpu()
+    L = 64 * 6
+    c = make_cache([L], 1, 64, cache, seed=61)
+    page = c["table"][0, 2]
+    code = 100 if cache == "int8" else 96.0
+    c["k"][page] = torch.full(c["k"][page].shape, code).to(c["k"].dtype)
+    q = (torch.ones((1, 4, D)) + 0.1 * torch.randn((1, 4, D), generator=torch.Generator().manual_seed(62))).bfloat16().cuda()
+    c["ks"][page] = 60 / (code * D * SCALE)
+    c["vs"][page] = 0.0
+    seen = [[np.ones(L, dtype=bool)]]
+    out, lse = run_list(c, q, [[list(range(6))]], splits)
+    assert out.abs().max() > 0
+    check_far(c, q, seen, out, lse, splits)

@@ -11,6 +11,7 @@ from block_sparse_attention_step_b200 import seer
 from oracle import cache_oracle as C
 from oracle import seer_oracle as O
 
+import test_gpu_cache_decode as decode
 from gpu_util import MARGIN, require_gpu
 
 D = 128
@@ -244,3 +245,36 @@ def test_append_prefill_and_decode_far_into_a_pool(cache):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert got[0][-1].item() == 0 and got[0][-2].abs().max() > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cache", ["e4m3", "int8"])
+@pytest.mark.parametrize("sizes", [(1e-36,), (1e-30, 1.0), (1e33,), (1.0, 1e-36, 1e30, 0.0), (1e-30, 0.0)])
+def test_decodes_read_whatever_scales_the_append_writes(cache, sizes):
+    """Values from 1e-36 to 1e33, block by block, through the append and both decodes: out and lse against fp64 over the
+    cache as it is held, and nothing flagged."""
+    require_gpu()
+    Hq, Hkv, bs, blocks, L = 8, 2, 64, 8, 64 * 7 + 5
+    g = torch.Generator().manual_seed(31)
+    q, k, v = rows(L, Hq, Hkv, g)
+    v = (v.float() * torch.tensor([sizes[t // bs % len(sizes)] for t in range(L)], device="cuda")[:, None, None]).bfloat16()
+    dtype = torch.float8_e4m3fn if cache == "e4m3" else torch.int8
+    kp, vp = [torch.zeros((blocks + 2, bs, Hkv, D), device="cuda").to(dtype) for _ in range(2)]
+    ks, vs = [torch.full((blocks + 2, Hkv), float("nan"), device="cuda") for _ in range(2)]
+    table = torch.randperm(blocks + 2, generator=g)[:blocks].int()[None]
+    d = seer.make_dims(1, Hq, Hkv, D, bs, blocks, blocks + 2)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    seer.seer_append_rope(d, seer.append_args(k, v, kp, vp, table.cuda(), torch.tensor([L], dtype=torch.int32).cuda(),
+                                              cu_tokens=torch.tensor([0, L], dtype=torch.int32).cuda(), max_new=L, k_scale=ks, v_scale=vs, dev_status=status))
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    c = {"k": kp.cpu(), "v": vp.cpu(), "ks": ks.cpu(), "vs": vs.cpu(), "cache": cache, "layout": "nhd", "bs": bs, "lens": [L], "Hkv": Hkv, "table": table,
+         "nbmax": blocks, "pages": blocks + 2, "nb": [blocks]}
+    one = q[-1:].contiguous()
+    for splits in (1, 3, 16):
+        chosen = [[[0, 1, 2, 5, 7], list(range(blocks))]]
+        seen = [[np.isin(np.arange(L) // bs, x) for x in chosen[0]]]
+        out, lse = decode.run_list(c, one, chosen, splits)
+        decode.check_far(c, one, seen, out, lse, splits)
+        out, lse, _ = decode.run_window(c, one, 300, 40, splits)
+        decode.check_far(c, one, [[C.window_seen(L - 1, L, 300, 40)] * Hkv], out, lse, splits)
