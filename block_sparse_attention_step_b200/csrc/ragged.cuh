@@ -48,7 +48,7 @@ struct Seq {
 };
 
 // n = 0: nothing to do (an inactive slot, or offsets and lengths that do not
-// fit, which are flagged).
+// fit, which are flagged); its L is 0, whatever length the slot holds.
 __device__ __forceinline__ Seq load_seq(const int32_t* cu, const int32_t* seqlens, int b, int T,
                                         int max_new, int capacity, int32_t* status) {
   Seq s;
@@ -69,6 +69,7 @@ __device__ __forceinline__ Seq load_seq(const int32_t* cu, const int32_t* seqlen
     flag_status(status, SEER_DEV_BAD_TOKENS);
     s.n = 0;
   }
+  if (s.n == 0) s.L = 0;
   return s;
 }
 

@@ -442,3 +442,37 @@ def test_large_values_that_a_query_does_not_see_weigh_nothing(window, sinks, bs,
                 # weights and out rounded to bf16 (2^-8 each); 1e-4 for scores of this size
                 tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 1e-4) * (w @ np.abs(v[seen][:, clean]) + np.abs(want))
                 assert (np.abs(got[i, qh, clean] - want) <= tol).all(), (i, qh, np.abs(got[i, qh, clean] - want).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("slot", [0, 1, 2])
+@pytest.mark.parametrize("length", [-2 ** 31, -2 ** 31 + 70, -2 ** 31 + 71, -2 ** 31 + 100, -2 ** 31 + 101, -1, 2 ** 31 - 1])
+def test_length_of_a_slot_without_new_tokens_does_not_matter(length, slot):
+    """Windows of 70 whose difference from the length passes 32 bits: the other sequences' rows have the bits that they
+    have beside a slot of length 0, through the append and the prefill."""
+    require_gpu()
+    past, new = [10, 300, 63], [40, 90, 2]
+    past[slot] = new[slot] = 0
+    c = make_cache([p + n for p, n in zip(past, new)], 2, 64, "bf16", seed=slot)
+    c["k"], c["v"] = [torch.nan_to_num(c[n]) for n in "kv"]
+    T, Hq, Hkv = sum(new), 8, 2
+    g = torch.Generator().manual_seed(slot)
+    q, k, v = [torch.randn((T, h, D), generator=g).bfloat16().cuda() for h in (Hq, Hkv, Hkv)]
+    cu = torch.tensor([sum(new[:i]) for i in range(4)], dtype=torch.int32).cuda()
+    got = []
+    for at in (0, length):
+        lens = list(c["lens"])
+        lens[slot] = at
+        seqlens, table = torch.tensor(lens, dtype=torch.int32).cuda(), c["table"].cuda()
+        d = seer.make_dims(3, Hq, Hkv, D, 64, c["nbmax"], c["pages"])
+        kp, vp, status = on_gpu(c, "k"), on_gpu(c, "v"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        qr, out, lse = torch.empty_like(q), torch.full_like(q, 7), torch.full((Hq, T), 7.0, device="cuda")
+        kbar = torch.full((3, Hkv, c["nbmax"], D), 9.0, device="cuda")
+        seer.seer_append_rope(d, seer.append_args(k, v, kp, vp, table, seqlens, q=q, q_out=qr, rope=seer.seer_rope_table(512, 128), cu_tokens=cu,
+                                                  max_new=max(new), kbar=kbar, dev_status=status))
+        seer.seer_window_prefill(d, seer.window_prefill_args(qr, kp, vp, table, seqlens, cu_tokens=cu, max_new=max(new), window=70, sinks=3,
+                                                             softmax_scale=SCALE, out=out, lse_out=lse, dev_status=status))
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        got.append((qr, kp, vp, kbar, out, lse))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and (got[1][4] != 7).any((1, 2)).all()
