@@ -479,16 +479,53 @@ def seer_prefill(d, q, k_pool, v_pool, page_table, seqlens, w_gate, kbar, *, poo
 
 
 # ------------------------------------------------------------ paged KV cache
-def _keep(a, *tensors):
-    """Argument blocks of the cache operators hold on to their tensors and
-    remember the device these are on."""
-    live = [t for t in tensors if t is not None]
-    devices = {t.device for t in live}
+def _keep(a, **tensors):
+    """Argument blocks of the cache operators hold on to their tensors, by name,
+    and remember the device these are on."""
+    live = {name: t for name, t in tensors.items() if t is not None}
+    devices = {t.device for t in live.values()}
     if len(devices) > 1:
         raise ValueError(f"tensors on more than one device: {sorted(map(str, devices))}")
     a.tensors = live
     a.device = devices.pop().index
+    a.fits = None  # the dims and arguments that the tensors were last found to fit
     return a
+
+
+def _elements(d, a):
+    """Elements that an operator may touch of each tensor of its argument block."""
+    B, Hq, Hkv, D, blocks = d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, d.max_blocks
+    pool = ((d.num_pages - 1) * d.stride_page + (d.block_size - 1) * d.stride_token
+            + (Hkv - 1) * d.stride_head + D)
+    need = dict(k_pool=pool, v_pool=pool, k_scale=d.num_pages * Hkv, v_scale=d.num_pages * Hkv,
+                page_table=B * blocks, seqlens=B, cu_tokens=B + 1, dev_status=1)
+    if isinstance(a, seer_cache_attn_args):
+        rows = B
+        need.update(idx=B * Hkv * a.k_max, n_sel=B * Hkv, lse_out=B * Hq,
+                    workspace=0)  # the library checks its bytes
+    else:
+        rows = a.total_tokens
+        need.update(positions=rows, kbar=B * Hkv * blocks * D, lse_out=Hq * rows,
+                    rope=getattr(a, "max_position", 0) * getattr(a, "rotary_dim", 0))
+    need.update(q=rows * Hq * D, q_out=rows * Hq * D, out=rows * Hq * D, k_new=rows * Hkv * D,
+                v_new=rows * Hkv * D)
+    return need
+
+
+def _check_sizes(fn: str, d, a):
+    """No tensor is smaller than the dims and the other arguments say: the
+    kernels take their word for it."""
+    need = _elements(d, a)
+    for name, t in a.tensors.items():
+        if t.numel() < need[name]:
+            raise ValueError(f"{fn}: {name} has {t.numel()} elements, the dims ask for {need[name]}")
+    if isinstance(a, seer_append_args):  # rows may be strided: their heads have to be the dims' own
+        for name, heads in (("q", d.num_q_heads), ("q_out", d.num_q_heads),
+                            ("k_new", d.num_kv_heads), ("v_new", d.num_kv_heads)):
+            t = a.tensors.get(name)
+            if t is not None and tuple(t.shape[1:]) != (heads, d.head_dim):
+                raise ValueError(f"{fn}: {name} is {list(t.shape)}, the dims ask for "
+                                 f"[tokens][{heads}][{d.head_dim}]")
 
 
 def _call(fn: str, d, a, stream):
@@ -496,6 +533,10 @@ def _call(fn: str, d, a, stream):
     device = torch.cuda.current_device()
     if a.device != device:
         raise ValueError(f"{fn}: tensors on cuda:{a.device}, current device is cuda:{device}")
+    asked = (bytes(d), bytes(a))
+    if a.fits != asked:  # once for each content of the two: a call per step repeats them
+        _check_sizes(fn, d, a)
+        a.fits = asked
     raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
     status = getattr(_lib_handle or _lib(), fn)(ctypes.byref(d), ctypes.byref(a), raw)
     if status != SEER_OK:
@@ -587,8 +628,10 @@ def append_args(k_new, v_new, k_pool, v_pool, page_table, seqlens, *, q=None, q_
     a.seqlens = _ptr(seqlens, torch.int32, "seqlens")
     a.kbar = _ptr(kbar, torch.float32, "kbar", allow_none=True)
     a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
-    return _keep(a, k_new, v_new, k_pool, v_pool, page_table, seqlens, q, q_out, rope, cu_tokens,
-                 positions, k_scale, v_scale, kbar, dev_status)
+    return _keep(a, k_new=k_new, v_new=v_new, k_pool=k_pool, v_pool=v_pool, page_table=page_table,
+                 seqlens=seqlens, q=q, q_out=q_out, rope=rope, cu_tokens=cu_tokens,
+                 positions=positions, k_scale=k_scale, v_scale=v_scale, kbar=kbar,
+                 dev_status=dev_status)
 
 
 def seer_append_rope(d, args: seer_append_args, stream=None):
@@ -609,7 +652,7 @@ def seer_split_workspace_bytes(d, num_splits: int) -> int:
 
 
 def _cache_attn(q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, num_splits, workspace,
-                softmax_scale, out, lse_out, dev_status, *more):
+                softmax_scale, out, lse_out, dev_status, **more):
     a = seer_cache_attn_args()
     a.q = _ptr(q, torch.bfloat16, "q")
     _cache(a, k_pool, v_pool, k_scale, v_scale)
@@ -623,8 +666,9 @@ def _cache_attn(q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, num_sp
     a.out = _ptr(out, torch.bfloat16, "out")
     a.lse_out = _ptr(lse_out, torch.float32, "lse_out", allow_none=True)
     a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
-    return _keep(a, q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, workspace, out,
-                 lse_out, dev_status, *more)
+    return _keep(a, q=q, k_pool=k_pool, v_pool=v_pool, page_table=page_table, seqlens=seqlens,
+                 k_scale=k_scale, v_scale=v_scale, workspace=workspace, out=out, lse_out=lse_out,
+                 dev_status=dev_status, **more)
 
 
 def sparse_decode_q8_args(q, k_pool, v_pool, page_table, seqlens, idx, n_sel, *, k_scale, v_scale,
@@ -632,7 +676,7 @@ def sparse_decode_q8_args(q, k_pool, v_pool, page_table, seqlens, idx, n_sel, *,
                           dev_status=None) -> seer_cache_attn_args:
     """Arguments of seer_sparse_decode_q8 (float8_e4m3fn or int8 pools)."""
     a = _cache_attn(q, k_pool, v_pool, page_table, seqlens, k_scale, v_scale, num_splits,
-                    workspace, softmax_scale, out, lse_out, dev_status, idx, n_sel)
+                    workspace, softmax_scale, out, lse_out, dev_status, idx=idx, n_sel=n_sel)
     a.idx = _ptr(idx, torch.int32, "idx")
     a.n_sel = _ptr(n_sel, torch.int32, "n_sel")
     a.k_max = int(k_max)
@@ -680,7 +724,8 @@ def window_prefill_args(q, k_pool, v_pool, page_table, seqlens, *, window, sinks
     a.out = _ptr(out, torch.bfloat16, "out")
     a.lse_out = _ptr(lse_out, torch.float32, "lse_out", allow_none=True)
     a.dev_status = _ptr(dev_status, torch.int32, "dev_status", allow_none=True)
-    return _keep(a, q, k_pool, v_pool, cu_tokens, page_table, seqlens, out, lse_out, dev_status)
+    return _keep(a, q=q, k_pool=k_pool, v_pool=v_pool, cu_tokens=cu_tokens, page_table=page_table,
+                 seqlens=seqlens, out=out, lse_out=lse_out, dev_status=dev_status)
 
 
 def seer_window_prefill(d, args: seer_window_prefill_args, stream=None):

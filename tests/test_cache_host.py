@@ -164,3 +164,120 @@ def test_window_by_hand():
     assert C.window_seen(5, 8, 3, 1).tolist() == [True, False, False, True, True, True, False, False]
     assert C.window_seen(1, 4, 9, 0).tolist() == [True, True, False, False]
     assert C.window_seen(3, 4, 1, 2).tolist() == [True, True, False, True]
+
+
+# ------------------------------------------------- sizes against the dims
+class Sized:
+    """Stands for a device tensor: what the binding's checks ask of one."""
+
+    is_cuda, device = True, torch.device("cuda", 0)
+
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, shape
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return math.prod(self.shape[i + 1:])
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 16 * id(self)
+
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def fitting(op):
+    """Tensors that just fit dims(): B 2, 8 / 2 heads, 4 blocks of 64, 8 pages; 5 rows of new tokens."""
+    pool = {"k_pool": Sized(BF, 8, 64, 2, 128), "v_pool": Sized(BF, 8, 64, 2, 128)}
+    if op in ("sparse_decode_q8", "append_q8"):
+        pool = {"k_pool": Sized(torch.int8, 8, 64, 2, 128), "v_pool": Sized(torch.int8, 8, 64, 2, 128), "k_scale": Sized(F32, 8, 2), "v_scale": Sized(F32, 8, 2)}
+    t = {**pool, "page_table": Sized(I32, 2, 4), "seqlens": Sized(I32, 2), "dev_status": Sized(I32, 1)}
+    if op.startswith("append"):
+        t.update(k_new=Sized(BF, 5, 2, 128), v_new=Sized(BF, 5, 2, 128), q=Sized(BF, 5, 8, 128), q_out=Sized(BF, 5, 8, 128), rope=Sized(F32, 100, 64),
+                 cu_tokens=Sized(I32, 3), positions=Sized(I32, 5), kbar=Sized(F32, 2, 2, 4, 128))
+        return t, dict(max_new=3)
+    if op == "window_prefill":
+        t.update(q=Sized(BF, 5, 8, 128), out=Sized(BF, 5, 8, 128), lse_out=Sized(F32, 8, 5), cu_tokens=Sized(I32, 3))
+        return t, dict(max_new=3, window=10, sinks=2, softmax_scale=0.1)
+    t.update(q=Sized(BF, 2, 8, 128), out=Sized(BF, 2, 8, 128), lse_out=Sized(F32, 2, 8))
+    if op == "window_decode":
+        return t, dict(window=10, sinks=2, num_splits=1, softmax_scale=0.1)
+    t.update(idx=Sized(I32, 2, 2, 3), n_sel=Sized(I32, 2, 2))
+    return t, dict(k_max=3, num_splits=1, softmax_scale=0.1)
+
+
+OPS = ["append", "append_q8", "sparse_decode_q8", "window_decode", "window_prefill"]
+
+
+def block_of(op, t, more):
+    return getattr(seer, op.replace("append_q8", "append") + "_args")(**t, **more)
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_tensors_smaller_than_the_dims_are_refused(lib, op):
+    d = dims()
+    t, more = fitting(op)
+    seer._check_sizes(op, d, block_of(op, t, more))                    # just large enough
+    for name in t:
+        shape = t[name].shape
+        for less in {(shape[0] - 1,) + shape[1:], shape[:-1] + (shape[-1] - 1,)}:
+            small = {**t, name: Sized(t[name].dtype, *less)}
+            if name == "k_new":
+                small["v_new"] = Sized(BF, *less)
+            if name in ("q", "q_out") and op.startswith("append"):
+                small["q"], small["q_out"] = Sized(BF, *less), Sized(BF, *less)
+            rows_are_ours = name in ("q", "k_new") and op in ("append", "append_q8", "window_prefill")
+            if name == "rope" or (rows_are_ours and less[0] != shape[0]):
+                continue                                               # these say themselves how many rows there are
+            with pytest.raises(ValueError):
+                seer._check_sizes(op, d, block_of(op, small, more))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("change", [dict(batch=5), dict(max_blocks=5), dict(num_pages=9), dict(num_q_heads=10), dict(num_kv_heads=4), dict(block_size=128),
+                                    dict(stride_page=64 * 2 * 128 + 16), dict(stride_token=512)])
+def test_larger_dims_than_the_tensors_are_refused(lib, op, change):
+    t, more = fitting(op)
+    a = block_of(op, t, more)
+    with pytest.raises(ValueError, match=op):
+        seer._check_sizes(op, dims(**change), a)
+
+
+def test_heads_that_only_add_up_are_refused(lib):
+    t, more = fitting("append")
+    for name in ("q", "k_new"):
+        other = "q_out" if name == "q" else "v_new"
+        shape = (10, t[name].shape[1] // 2, 128)
+        with pytest.raises(ValueError):
+            seer._check_sizes("append", dims(), block_of("append", {**t, name: Sized(BF, *shape), other: Sized(BF, *shape)}, more))
+    # tables and outputs made for a larger batch stay allowed
+    t, more = fitting("window_decode")
+    t.update(page_table=Sized(I32, 5, 4), seqlens=Sized(I32, 5), out=Sized(BF, 5, 8, 128), k_pool=Sized(BF, 9, 64, 2, 128))
+    seer._check_sizes("window_decode", dims(), block_of("window_decode", t, more))
+
+
+def test_a_call_checks_sizes_before_anything_else_and_again_when_something_changed(lib, monkeypatch):
+    t, more = fitting("window_decode")
+    a, d = block_of("window_decode", t, more), dims()
+    calls = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(seer, "_lib_handle", type("Lib", (), {"seer_window_decode": staticmethod(lambda *x: calls.append(x) or 0)}))
+    for _ in range(2):
+        seer.seer_window_decode(d, a, 0)
+    assert len(calls) == 2
+    d.batch = 5
+    with pytest.raises(ValueError, match="seer_window_decode: q has 2048 elements"):
+        seer.seer_window_decode(d, a, 0)
+    d.batch = 2
+    seer.seer_window_decode(d, a, 0)
+    a.k_max = 7                                                         # of the other form: asks for no tensor here
+    seer.seer_window_decode(d, a, 0)
+    assert len(calls) == 4

@@ -278,3 +278,25 @@ def test_decodes_read_whatever_scales_the_append_writes(cache, sizes):
         decode.check_far(c, one, seen, out, lse, splits)
         out, lse, _ = decode.run_window(c, one, 300, 40, splits)
         decode.check_far(c, one, [[C.window_seen(L - 1, L, 300, 40)] * Hkv], out, lse, splits)
+
+
+@pytest.mark.gpu
+def test_calls_whose_tensors_are_too_small_launch_nothing():
+    require_gpu()
+    s = Server("bf16", seed=9)
+    s.append([70, 3, 64])
+    k, v, table = s.kp.clone(), s.vp.clone(), s.table[:, :-1].contiguous()
+    q, new_k, new_v = rows(3, s.Hq, s.Hkv, s.g)
+    out = torch.full((s.B, s.Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="page_table"):
+        seer.seer_append_rope(s.d, seer.append_args(new_k, new_v, s.kp, s.vp, table, s.seqlens))
+    with pytest.raises(ValueError, match="positions"):
+        seer.seer_append_rope(s.d, seer.append_args(new_k, new_v, s.kp, s.vp, s.table, s.seqlens, rope=s.rope, positions=s.seqlens[:2]))
+    with pytest.raises(ValueError, match="seqlens"):
+        seer.seer_window_decode(s.d, seer.window_decode_args(q.contiguous(), s.kp, s.vp, s.table, s.seqlens[:2], window=9, sinks=0, num_splits=1, softmax_scale=SCALE,
+                                                             out=out))
+    with pytest.raises(ValueError, match="lse_out"):
+        seer.seer_window_prefill(s.d, seer.window_prefill_args(q.contiguous(), s.kp, s.vp, s.table, s.seqlens, window=9, sinks=0, softmax_scale=SCALE, out=out,
+                                                               lse_out=torch.zeros(2, device="cuda")))
+    torch.cuda.synchronize()
+    assert torch.equal(k, s.kp) and torch.equal(v, s.vp) and (out == 7).all() and s.status.item() == 0
