@@ -300,3 +300,52 @@ def test_calls_whose_tensors_are_too_small_launch_nothing():
                                                                lse_out=torch.zeros(2, device="cuda")))
     torch.cuda.synchronize()
     assert torch.equal(k, s.kp) and torch.equal(v, s.vp) and (out == 7).all() and s.status.item() == 0
+
+
+@pytest.mark.gpu
+def test_append_prefill_append_and_decode_without_a_wait():
+    """A chunk's append and prefill, single tokens' append and decode, and prefills and decodes one behind the other over
+    one bf16 cache, 20 rounds enqueued at once: rotated queries, outputs, lse, pooled keys and pages have the bits that
+    they have with a wait after every call.  (The prefill lets its successor start before its own predecessor has ended.)"""
+    require_gpu()
+    s = Server("bf16", B=2, Hq=8, Hkv=2, seed=15)
+    s.append([64, 100])
+    lens, calls, held = list(s.lens), [], []
+
+    def empty(*shape, dtype=torch.float32):
+        held.append(torch.empty(shape, dtype=dtype, device="cuda"))
+        return held[-1]
+
+    for i in range(20):
+        for new in ([3 + 5 * (i % 4), 1 + i % 3], [1, 1]):
+            T = sum(new)
+            lens = [x + n for x, n in zip(lens, new)]
+            seqlens = torch.tensor(lens, dtype=torch.int32).cuda()
+            cu = torch.tensor([0, new[0], T], dtype=torch.int32).cuda()
+            q, k, v = rows(T, s.Hq, s.Hkv, s.g)
+            qr = empty(T, s.Hq, D, dtype=torch.bfloat16)
+            a = seer.append_args(k, v, s.kp, s.vp, s.table, seqlens, q=q, q_out=qr, rope=s.rope, cu_tokens=cu, max_new=max(new),
+                                 kbar=s.kbar if i % 2 else None, dev_status=s.status)
+            pre = [seer.window_prefill_args(qr, s.kp, s.vp, s.table, seqlens, cu_tokens=cu, max_new=max(new), window=w, sinks=4, softmax_scale=SCALE,
+                                            out=empty(T, s.Hq, D, dtype=torch.bfloat16), lse_out=empty(s.Hq, T), dev_status=s.status) for w in (90, 300)]
+            calls.append((seer.seer_append_rope, a))
+            if new == [1, 1]:
+                w = seer.window_decode_args(qr, s.kp, s.vp, s.table, seqlens, window=90, sinks=4, num_splits=1 + i % 3, softmax_scale=SCALE,
+                                            out=empty(2, s.Hq, D, dtype=torch.bfloat16), lse_out=empty(2, s.Hq), dev_status=s.status)
+                calls += [(seer.seer_window_decode, w), (seer.seer_window_prefill, pre[0])][:: 1 if i % 2 else -1]
+            else:
+                calls += [(seer.seer_window_prefill, x) for x in pre[: 1 + i % 2]]
+    written = [s.kp, s.vp, s.kbar] + held
+    start = [x.clone() for x in written]
+    torch.cuda.synchronize()
+    for fn, a in calls:                                 # at once
+        fn(s.d, a)
+    torch.cuda.synchronize()
+    first = [x.clone() for x in written]
+    for x, y in zip(written, start):
+        x.copy_(y)
+    for fn, a in calls:                                 # one by one
+        fn(s.d, a)
+        torch.cuda.synchronize()
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(first, written)) and s.status.item() == 0
+    assert any(not torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(first, start))
