@@ -37,10 +37,11 @@
 // pooled keys (950 MB, q by the row role, k and v by the block role) take 156 us,
 // 6.1 TB/s, 0.94 of a plain copy's rate; a kernel for each role took 234.  With
 // codes a block's CTA loads, reduces and stores in turn and two of them fill an
-// SM: 8 ragged chunks of up to 2.5K tokens of 32 + 8 + 8 heads into an int8 cache
-// take 53 us, 4.4 TB/s (26 without q, whose rows stream at 6.2 TB/s).  A single
-// token for each of 64 sequences takes 5.8 us, all of it launch and loads that
-// depend on one another.
+// SM, the row role's among them: 8 ragged chunks of up to 2.5K tokens of 32 + 8 + 8
+// heads into 128-token pages take 53 us with e4m3 codes and 54 with int8, 4.4 TB/s
+// (25 and 26 without q, whose rows would take 27 alone; pages of 64: 50 and 53).
+// A single token for each of 64 sequences takes 5.9 us (int8 6.3), all of it launch
+// and loads that depend on one another.
 #include <cuda_fp16.h>
 
 #include "block_mean.cuh"
@@ -107,8 +108,10 @@ struct Code8<SEER_CACHE_INT8> {
       return code(a) | (code(b) << 8) | (code(c) << 16) | (code(d) << 24);
     }
     // |x| <= 127 (and a rounding): 1.5 * 2^23 + x rounds x to the nearest integer,
-    // ties to even, whose two's complement is the sum's low byte (converting
-    // instructions run at a quarter of the rate)
+    // ties to even, whose two's complement is the sum's low byte.  Against converting
+    // instructions here and in the pooled sums: the chunks of 128-token pages 26.5 us
+    // instead of 27.6 without q and 53.9 either way with it, of 64-token pages 52.9
+    // instead of 51.9
     const uint64_t magic = pack2(12582912.f, 12582912.f);
     unpack2(add2(ab, magic), a, b);
     unpack2(add2(cd, magic), c, d);
@@ -700,8 +703,9 @@ __device__ __forceinline__ void block_role(const AppendParams& p, const Touched&
         a.w += __uint_as_float(w.y & 0xffff0000u);
       }
     } else {
-      // sums of at most 128 codes are exact (e4m3: multiples of 2^-9 below 2^16), so
-      // the scale is applied once
+      // the scale is applied once, to the sum of codes.  A warp's part, at most 16 rows,
+      // is exact (e4m3: multiples of 2^-9 below 2^13), and so is the sum of a block of
+      // 64; the parts of 128 rows of e4m3 codes may pass 2^15 and round to fp32
       a = make_float4(0.f, 0.f, 0.f, 0.f);
       // dims 4 lane .. 4 lane + 3: half of the codes in the first half of chunk lane / 2
       const uint32_t* w = reinterpret_cast<const uint32_t*>(sh.keys) + (lane >> 1) * 4 + (lane & 1);
@@ -740,7 +744,7 @@ __global__ void __launch_bounds__(BS * 4, BS == 64 ? 4 : 2) append_blocks_kernel
   pdl_launch_dependents();
   // the block CTAs, spread evenly over the grid: they wait for loads, barriers and
   // arithmetic in turn while the row CTAs stream (2 x 16K prompt 156 us, all
-  // of them first 164, last 160; int8 chunks alike)
+  // of them first 164, last 160; e4m3 chunks alike)
   const int before = (int)((uint64_t)blockIdx.x * p.block_share >> 32);
   const bool is_block = (int)((uint64_t)(blockIdx.x + 1) * p.block_share >> 32) > before;
   if (is_block) {
@@ -822,7 +826,6 @@ cudaError_t run_append_rope(AppendParams p, int cache, int num_sms, cudaStream_t
   int64_t items = p.B * per_seq;
   const int64_t by_rows = (int64_t)p.T / p.bs + 2 * (int64_t)p.B;
   if (p.max_new > 1 && by_rows < items) items = by_rows;
-  p.items = (int)items;
   // heads of a block per CTA: as many as leave the SMs' resident CTAs twice
   // over (finding the block and its page are paid once for them)
   p.heads = 1;

@@ -80,12 +80,14 @@ constexpr int kClusterMax = 8;  // CTAs that join one row's pieces without a par
 // a combine.  A stage of a lone CTA takes 0.41 us; a piece's start and join
 // (launch, three dependent loads, the first copy, the cluster) about 11 of
 // them.  Measured, pieces 1 / 2 / 3 / 4 / 8 (us):
-//   128 rows of 52 stages, e4m3     30.0 / 27.3 / 27.3 / 35.5 / 39.0   rule: 3
-//   256 rows of 58, e4m3            51.2 / 68.8 / 57.9 / 62.9          rule: 1
-//   512 rows of 58, e4m3           117.5 / 106.5 / 105.2 / 110.4       rule: 2
-//   512 ragged rows to 104, int8   116.0 / 106.4 / 109.9 / 118         rule: 2
-//   512 ragged rows to 66, bf16      146 / 156 / 158 / 160 / 202       rule: 1
-//   1 row of 8, e4m3                 8.3 / 7.1 / 6.5 / 5.4 / 4.9       rule: 8
+//   128 rows of 52 stages, e4m3     30.1 / 28.5 / 28.2 / 37.3 / 40.9   rule: 3
+//   256 rows of 58, e4m3            51.3 / 67.9 / 57.1 / 62.0          rule: 1
+//   512 rows of 58, e4m3           126.8 / 106.2 / 104.9 / 108.1       rule: 2
+//   512 ragged rows to 104, int8   116.5 / 106.6 / 113.8 / 121.6       rule: 2
+//   512 ragged rows to 66, bf16      146 / 157 / 160 / 164 / 205       rule: 1
+//   1 row of 8, e4m3                 8.5 / 7.1 / 6.7 / 5.8 / 5.1       rule: 8
+// (the window's helper does not know the cache type and takes bf16's two CTAs per
+// SM, also for 8-bit caches, of which three fit)
 constexpr int kPieceStart = 11, kCombineStages = 5;
 
 int ctas_per_sm(const seer_dims* d, int cache) {
@@ -94,7 +96,7 @@ int ctas_per_sm(const seer_dims* d, int cache) {
 
 // Whether the rows go out longest sequence first: where they do not all fit on
 // the SMs at once, so that the last to start are short (64 ragged sequences of 4K
-// to 32K x 8 heads, int8: 106 us, in the order they come 112).  Ranking costs a
+// to 32K x 8 heads, int8: 6 us less than the 112 in the order they come).  Ranking costs a
 // CTA half a microsecond, which window rows, mostly as long as the window, do
 // not get back (147.5 against 146.9).
 bool longest_first(const seer_dims* d, int32_t splits, int per_sm) {

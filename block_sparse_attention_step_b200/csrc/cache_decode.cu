@@ -39,7 +39,7 @@
 // rescaling of O or l in between.  Bound by HBM: 256 B (bf16: 512) per token and KV head.
 // bf16, 64 sequences x 8 heads, window 4096: 146 us, 6.7 TB/s.  8 bit: 128-byte
 // rows 1 KB apart (token-major pages of 8 heads) are what bounds it; the copies
-// without the math take 25.3 of 28.4 us (16 x 32K tokens, 10 % of the blocks,
+// without the math take 25.3 of 28.3 us (16 x 32K tokens, 10 % of the blocks,
 // 109 MB) and 95.6 of 108 us (64 ragged sequences, 485 MB).  The second reference
 // and exponential of a token, without which l lost tokens whose V scale is 2^100
 // below another's, are 0.8 and 1.5 us of these.  One row of 512 tokens takes

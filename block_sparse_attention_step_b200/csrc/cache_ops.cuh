@@ -30,7 +30,6 @@ struct AppendParams {
   int rows_kv;      // the row role writes k and v too (bf16, no pooled keys)
   int tile_tokens;  // tokens of a row-role tile
   int segments, segment_rows;  // parts a token's rows are cut into, one warp each
-  int items;        // touched blocks at most
   int heads;        // KV heads of a block per CTA (divides Hkv)
   uint64_t block_share;  // 2^32 x block CTAs / all CTAs, rounded up
 };

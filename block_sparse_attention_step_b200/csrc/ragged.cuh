@@ -7,11 +7,9 @@
 
 namespace seer {
 
-// True in one lane of a converged warp.  Code under it is known to run in a
-// single thread, so the operands of tensor-core and TMA instructions stay in
-// uniform registers; under `lane == 0` the compiler issues each of them through
-// a loop over the active lanes (180 cycles per tcgen05.mma instead of the 64
-// that a 128 x 128 x 16 one takes).
+// True in one lane of a converged warp (elect.sync).  Tensor-core and TMA
+// instructions are issued under it: a tcgen05.mma of 128 x 128 x 16 took 180
+// cycles under `lane == 0` and 64 under this.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -20,10 +18,10 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // mbar_wait for kernels whose warps wait most of the time next to others that
-// are short of issue slots: no suspend-time hint, so the hardware holds the
-// warp until the phase completes or its own time limit passes (with a hint
-// the wait becomes a loop of polls and short sleeps: a third of all
-// instructions of the prefill).  Bounded like mbar_wait.
+// are short of issue slots: try_wait without a suspend-time hint, whose own time
+// limit decides how long the warp is held (with mbar_wait's hint a third of the
+// instructions that the prefill executed were the waits').  Bounded like
+// mbar_wait.
 __device__ __forceinline__ bool mbar_hold(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_u32(bar);
   long long t0 = 0;

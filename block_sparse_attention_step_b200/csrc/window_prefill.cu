@@ -31,8 +31,8 @@
 // Where there are too few row tiles for the SMs (a short chunk behind a long
 // context) the CTAs of a cluster take a part of a tile's keys each and join their
 // states (O, maximum, sum in fp32) over distributed shared memory.  8K prompt (40/8 heads, window 2048, 301
-// GFLOP): 363 us in a loop at the power limit, 329 in a burst (915 TFLOP/s); ragged
-// chunks of 129 to 2050 tokens (32/8 heads, window 1000): 91 to 102.  N 128 with two Q
+// GFLOP): 359 to 367 us in a loop at the power limit, 316 in a burst (952 TFLOP/s);
+// ragged chunks of 129 to 2050 tokens (32/8 heads, window 1000): 94 to 105.  N 128 with two Q
 // tiles per CTA and one CTA per SM took 364 to 398, and 17 us instead of 10.7 on a
 // chunk of 77 tokens.
 #include <cooperative_groups.h>
@@ -104,7 +104,7 @@ __device__ __forceinline__ uint64_t below(int n) {
 
 // The key tiles of a CTA whose rows lie at positions p_min .. p_max.
 struct WPKeysOf {
-  int p_min, p_max, window, sinks, L;
+  int p_min, p_max, window, sinks;
   int sink_tiles, first_tile, n;  // tile numbers 0 .. sink_tiles - 1, then first_tile ..
   int lo;                         // first of them that is this CTA's
 
@@ -118,12 +118,11 @@ struct WPKeysOf {
   }
 };
 
-__device__ __forceinline__ WPKeysOf wp_keys(int p_min, int p_max, int window, int sinks, int L) {
+__device__ __forceinline__ WPKeysOf wp_keys(int p_min, int p_max, int window, int sinks) {
   WPKeysOf k;
   k.p_min = p_min;
   k.p_max = p_max;
   k.window = window;
-  k.L = L;
   k.sinks = min(sinks, p_max + 1);
   k.sink_tiles = ceil_div_i(k.sinks, kWPKeys);
   k.first_tile = max(k.sink_tiles, max(0, p_min - window + 1) / kWPKeys);
@@ -218,14 +217,21 @@ __global__ void __launch_bounds__(kWPThreads, 2)
 
   // ---- which sequence and which of its token tiles (warp 0); meanwhile
   // tensor memory (warp 1), barriers (warp 2), tensor maps (warp 3)
+  // The successor may start here, ahead of this grid's tensor memory: its CTAs could
+  // hold columns that a CTA of this grid still has to get, and wait for this grid
+  // to end.  They cannot as long as no more than two CTAs with tensor memory (256
+  // columns each, of 512) fit on an SM by their shared memory: 113 KB here, and
+  // prefill_attention_kernel, which is of that size too, is launched without the
+  // programmatic attribute.  A kernel with more columns or less shared memory has
+  // to move this behind tmem_alloc.
   pdl_launch_dependents();
   if (warp == 0) {
     pdl_wait();  // every other read of global memory comes after the barrier below
     // Row tiles that see a whole window first (whatever their order), then those
     // near the start of their sequence, the longest of each first, so that the
     // grid ends with short CTAs (full causal prompts of 2K / 4K tokens, 32/8 heads:
-    // 45 / 136 us, in the order of the rows 53 / 149; ragged chunks 91, the other
-    // way round 97 to 104).
+    // 42 / 136 us, in the order of the rows 53 / 149; ragged chunks vary more from
+    // run to run, 94 to 105, than with the order).
     int found_b = -1, found_tile = 0;
     Seq found = {0, 0, 0};
     if (p.max_new == 1 && item < p.B) {  // a row tile per sequence
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(kWPThreads, 2)
   const int t0 = bars.tile * p.ntok;                       // first query token of the CTA
   const int last = min(t0 + p.ntok, seq.n) - 1;            // last query token
   const int pa = past + t0, pz = past + last;              // their positions
-  WPKeysOf keys = wp_keys(pa, pz, p.window, p.sinks, seq.L);
+  WPKeysOf keys = wp_keys(pa, pz, p.window, p.sinks);
   int nt = bars.stop ? 0 : keys.n;
   if constexpr (C > 1) {
     keys.lo = (int)((int64_t)piece * nt / C);

@@ -504,7 +504,9 @@ SEER_API seer_status seer_rope_table(int32_t max_position, int32_t rotary_dim,
  * already counts them, so token i lies at cache position seqlens[b] - n_b + i.
  * Rows behind the last sequence and those of a sequence whose offsets or
  * length do not fit (flagged SEER_DEV_BAD_TOKENS) are left out: nothing is
- * written for them.  A row whose page is outside the pool is left out too
+ * written for them.  cu_tokens does not decrease; where it does (flagged the
+ * same way), rows of the sequences around the step may be left out too.  The
+ * length of a sequence without new tokens does not matter.  A row whose page is outside the pool is left out too
  * (SEER_DEV_BAD_PAGE).
  *
  * The first rotary_dim dims of each q and k row are turned in pairs (x, y) ->
