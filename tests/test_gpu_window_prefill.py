@@ -476,3 +476,25 @@ def test_length_of_a_slot_without_new_tokens_does_not_matter(length, slot):
         assert status.item() == 0
         got.append((qr, kp, vp, kbar, out, lse))
     assert all(torch.equal(a, b) for a, b in zip(*got)) and (got[1][4] != 7).any((1, 2)).all()
+
+
+@pytest.mark.gpu
+def test_prefills_on_two_streams_at_once():
+    """A short chunk (keys split over clusters) on one stream and a long one on another, enqueued 12 times without a wait:
+    the bits of calls one by one."""
+    require_gpu()
+    runs = []
+    for seed, (past, new, Hkv) in enumerate((([700, 0], [40, 130], 2), ([100], [1500], 8))):
+        c = make_cache([p + n for p, n in zip(past, new)], Hkv, 64, "bf16", seed=seed)
+        runs.append(run(c, past, new, 4 * Hkv, 300, 5, seed=seed))
+    want = [(out.clone(), lse.clone()) for _, out, lse, _ in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _, out, lse, _ in runs:
+        out.fill_(7)
+        lse.fill_(7)
+    torch.cuda.synchronize()
+    for _ in range(12):
+        for (_, _, _, (d, a)), stream in zip(runs, streams):
+            seer.seer_window_prefill(d, a, stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, o) and torch.equal(lse, l) for (_, out, lse, _), (o, l) in zip(runs, want))
