@@ -1,7 +1,8 @@
 """ctypes binding of ``libseer.so`` (the C ABI in ``include/seer.h``).
 
 Argument marshalling only: every function takes torch tensors (device memory
-for the device arguments), checks dtype and contiguity, passes raw pointers
+for the device arguments), checks dtype and contiguity (the paged-cache
+operators also shapes against the dims), passes raw pointers
 and the current CUDA stream, and raises ``SeerError`` on a non-zero status.
 All computation happens in the library's kernels.  The library must have been
 built (``python -m block_sparse_attention_step_b200.build``); there is no
@@ -10,6 +11,7 @@ fallback path, a missing library raises at first use.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -492,40 +494,43 @@ def _keep(a, **tensors):
     return a
 
 
-def _elements(d, a):
-    """Elements that an operator may touch of each tensor of its argument block."""
+def _shapes(d, a):
+    """Shape that an operator takes each tensor of its argument block for (the
+    pools, which have strides of their own: elements)."""
     B, Hq, Hkv, D, blocks = d.batch, d.num_q_heads, d.num_kv_heads, d.head_dim, d.max_blocks
     pool = ((d.num_pages - 1) * d.stride_page + (d.block_size - 1) * d.stride_token
             + (Hkv - 1) * d.stride_head + D)
-    need = dict(k_pool=pool, v_pool=pool, k_scale=d.num_pages * Hkv, v_scale=d.num_pages * Hkv,
-                page_table=B * blocks, seqlens=B, cu_tokens=B + 1, dev_status=1)
+    shapes = dict(k_pool=(pool,), v_pool=(pool,), k_scale=(d.num_pages, Hkv),
+                  v_scale=(d.num_pages, Hkv), page_table=(B, blocks), seqlens=(B,),
+                  cu_tokens=(B + 1,), dev_status=(1,))
     if isinstance(a, seer_cache_attn_args):
         rows = B
-        need.update(idx=B * Hkv * a.k_max, n_sel=B * Hkv, lse_out=B * Hq,
-                    workspace=0)  # the library checks its bytes
+        shapes.update(idx=(B, Hkv, a.k_max), n_sel=(B, Hkv), lse_out=(B, Hq),
+                      workspace=(0,))  # the library checks its bytes
     else:
         rows = a.total_tokens
-        need.update(positions=rows, kbar=B * Hkv * blocks * D, lse_out=Hq * rows,
-                    rope=getattr(a, "max_position", 0) * getattr(a, "rotary_dim", 0))
-    need.update(q=rows * Hq * D, q_out=rows * Hq * D, out=rows * Hq * D, k_new=rows * Hkv * D,
-                v_new=rows * Hkv * D)
-    return need
+        shapes.update(positions=(rows,), kbar=(B, Hkv, blocks, D), lse_out=(Hq, rows),
+                      rope=(getattr(a, "max_position", 0), getattr(a, "rotary_dim", 0)))
+    shapes.update(q=(rows, Hq, D), q_out=(rows, Hq, D), out=(rows, Hq, D), k_new=(rows, Hkv, D),
+                  v_new=(rows, Hkv, D))
+    return shapes
 
 
 def _check_sizes(fn: str, d, a):
-    """No tensor is smaller than the dims and the other arguments say: the
-    kernels take their word for it."""
-    need = _elements(d, a)
+    """No tensor is smaller than the dims and the other arguments say (the
+    kernels take their word for it), and none has other inner extents.  One of
+    another number of dimensions counts by its elements."""
+    shapes = _shapes(d, a)
     for name, t in a.tensors.items():
-        if t.numel() < need[name]:
-            raise ValueError(f"{fn}: {name} has {t.numel()} elements, the dims ask for {need[name]}")
-    if isinstance(a, seer_append_args):  # rows may be strided: their heads have to be the dims' own
-        for name, heads in (("q", d.num_q_heads), ("q_out", d.num_q_heads),
-                            ("k_new", d.num_kv_heads), ("v_new", d.num_kv_heads)):
-            t = a.tensors.get(name)
-            if t is not None and tuple(t.shape[1:]) != (heads, d.head_dim):
-                raise ValueError(f"{fn}: {name} is {list(t.shape)}, the dims ask for "
-                                 f"[tokens][{heads}][{d.head_dim}]")
+        want, got = shapes[name], tuple(t.shape)
+        if t.numel() < math.prod(want):
+            raise ValueError(f"{fn}: {name} has {t.numel()} elements, the dims ask for "
+                             f"{math.prod(want)}")
+        rows = isinstance(a, seer_append_args) and name in ("q", "q_out", "k_new", "v_new")
+        for i in range(1, len(want) if len(got) == len(want) else 0):
+            # behind a single row another extent moves nothing (strided rows apart)
+            if got[i] != want[i] and (rows or math.prod(want[:i]) > 1):
+                raise ValueError(f"{fn}: {name} is {list(got)}, the dims ask for {list(want)}")
 
 
 def _call(fn: str, d, a, stream):

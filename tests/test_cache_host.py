@@ -281,3 +281,23 @@ def test_a_call_checks_sizes_before_anything_else_and_again_when_something_chang
     a.k_max = 7                                                         # of the other form: asks for no tensor here
     seer.seer_window_decode(d, a, 0)
     assert len(calls) == 4
+
+
+@pytest.mark.parametrize("op,name,shape", [
+    ("append", "page_table", (2, 6)), ("append", "kbar", (2, 2, 5, 128)), ("append_q8", "k_scale", (8, 3)), ("window_decode", "page_table", (2, 5)),
+    ("window_decode", "q", (2, 10, 128)), ("window_decode", "out", (2, 8, 256)), ("window_decode", "lse_out", (2, 9)), ("sparse_decode_q8", "idx", (2, 2, 4)),
+    ("sparse_decode_q8", "n_sel", (2, 3)), ("window_prefill", "lse_out", (8, 6)), ("window_prefill", "q", (5, 10, 128)), ("window_prefill", "page_table", (2, 8))])
+def test_tensors_of_other_inner_extents_are_refused(lib, op, name, shape):
+    """Larger, so every read is inside, but rows lie elsewhere; flat ones and a single row are taken as they come."""
+    t, more = fitting(op)
+    wide = {**t, name: Sized(t[name].dtype, *shape)}
+    if name == "q" and op == "window_prefill":
+        wide["out"] = wide["q"]
+    with pytest.raises(ValueError, match=name):
+        seer._check_sizes(op, dims(), block_of(op, wide, more))
+    if name != "q" or op == "window_decode":
+        seer._check_sizes(op, dims(), block_of(op, {**t, name: Sized(t[name].dtype, math.prod(shape))}, more))
+    if name in ("page_table", "lse_out") and op == "window_decode":
+        d = dims()
+        d.batch = 1
+        seer._check_sizes(op, d, block_of(op, wide, more))
